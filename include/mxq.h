@@ -118,7 +118,9 @@ int mxq_device_supported(int device);
 
 /* Synchronizes `stream`, then reads and clears the device error word.
  * Returns MXQ_ETIMEOUT if a bounded wait ran out since the last check,
- * MXQ_ECUDA if a CUDA error is pending, else MXQ_OK.  Host-blocking. */
+ * MXQ_EINVAL if a kernel met an index in device data outside its range (the
+ * calls that take offsets, slots or positions say which), MXQ_ECUDA if a CUDA
+ * error is pending, else MXQ_OK.  Host-blocking. */
 mxq_status mxq_check(void *stream);
 
 /* Diagnostics of the error path: launches one thread that waits, for at
@@ -611,6 +613,180 @@ mxq_status mxq_qlinear_routed(const void *x, int32_t xdtype, int64_t m, int64_t 
                               const uint8_t *fmt_table, int32_t n_layers, int32_t n_intervals, int32_t layer,
                               int32_t step, int32_t n_steps, void *y, int32_t ydtype, int32_t *fmt_used,
                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Linears of a mixture of experts: rows in expert order.                  */
+/* ---------------------------------------------------------------------- */
+
+/* A router gives every token topk experts.  The calls below run the experts'
+ * linears in the library's formats without moving a count to the host:
+ *   mxq_expert_plan        ids -> offsets and slot
+ *   mxq_quantize_grouped   tokens -> quantized rows in expert order
+ *   mxq_qlinear_grouped    rows in expert order x their expert's weight
+ *   mxq_expert_combine     each token's rows, weighted and added
+ * Expert order: rows [offsets[e], offsets[e + 1]) belong to expert e, its
+ * choices in token order; slot[t][i] is the row of token t's i-th choice, -1
+ * for a dropped one.  Buffers of rows have a capacity (tokens * topk) the
+ * host knows; rows at and beyond offsets[n_experts] are not read for any
+ * result and never written.
+ * Grouped MMA layout of the byte scales (MXFP8, MXFP4, NVFP4): as
+ * MXQ_LAYOUT_MMA, with the rows of every group beginning at a multiple of
+ * 128: row j of group g is scale row 128 * (sum over g' < g of
+ * ceil(rows of g' / 128)) + j - offsets[g].  Bytes of scale rows and columns
+ * that hold no scale are unspecified.  Codes and INT8_ROW scales are compact.
+ * A part of the experts: pass offsets + first, n_groups = count and the
+ * weight of those experts; slots outside [offsets[first],
+ * offsets[first + count]) are passed over.
+ * Limits: rows <= 2^22, 1 <= experts <= 512, 1 <= topk <= 32.
+ * Offsets are device data: ones outside [0, rows] or out of order are
+ * clamped, so that no access leaves the buffers, and reported by mxq_check()
+ * as MXQ_EINVAL. */
+
+/* Scratch bytes mxq_expert_plan needs for `rows` = tokens * topk choices. */
+mxq_status mxq_expert_plan_workspace_bytes(int64_t rows, int32_t n_experts, size_t *bytes);
+
+/* The plan of a routing: a stable counting sort by expert.
+ *   expert_ids: device, id_bits = 32 or 64 bit integers, rows of them (token
+ *     by token); ids outside [0, n_experts) are dropped choices.
+ *   offsets: device int32[n_experts + 1]; slot: device int32[rows].
+ *   workspace: device scratch of mxq_expert_plan_workspace_bytes (may be NULL
+ *     when that is 0); clobbered.
+ * The same ids give the same plan, bit for bit.
+ * Errors: MXQ_EINVAL (sizes, pointers, alignment), MXQ_ENOSPACE, MXQ_ECUDA. */
+mxq_status mxq_expert_plan(const void *expert_ids, int32_t id_bits, int64_t rows, int32_t n_experts,
+                           int32_t *offsets, int32_t *slot, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* Bytes of the scales mxq_quantize_grouped writes for a capacity of `rows`
+ * rows in n_groups groups: byte scales (rows / 128 + min(rows, n_groups)) *
+ * 128 rows of the padded scale columns, INT8_ROW 4 * rows, FP8_TENSOR 0.
+ * (Codes: mxq_codes_bytes.) */
+mxq_status mxq_grouped_scales_bytes(int32_t fmt, int64_t rows, int32_t n_groups, int64_t cols, size_t *bytes);
+
+/* Quantizes tokens into expert order: every token is read and coded once and
+ * its codes and scales written to the rows of all its choices, each bit as
+ * mxq_quantize writes it.
+ *   x: x_rows x cols fp32/bf16 device, 16-byte aligned.
+ *   fmt: MXFP8, MXFP4, NVFP4, INT8_ROW or FP8_TENSOR (INT4: MXQ_EUNSUPPORTED).
+ *   hadamard_b: as mxq_quantize.
+ *   offsets: device int32[n_groups + 1].
+ *   slot: device int32[x_rows][topk], or NULL: x is in expert order already
+ *     (topk == 1, row t is row t, x_rows <= rows; the second linear of an
+ *     expert's MLP).
+ *   rows: capacity of codes and scales.
+ *   codes, scales: device, mxq_codes_bytes / mxq_grouped_scales_bytes.
+ *   tensor_scale: device fp32 (NVFP4, FP8_TENSOR): that of the tokens with at
+ *     least one row.
+ *   workspace: device scratch of mxq_quantize_workspace_bytes (NVFP4,
+ *     FP8_TENSOR; else NULL); clobbered.
+ * Constraints as mxq_quantize.  Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED (fmt),
+ * MXQ_ENOSPACE, MXQ_ECUDA. */
+mxq_status mxq_quantize_grouped(const void *x, int32_t xdtype, int64_t x_rows, int64_t cols, int32_t fmt,
+                                int32_t hadamard_b, const int32_t *offsets, int32_t n_groups,
+                                const int32_t *slot, int32_t topk, int64_t rows, void *codes, void *scales,
+                                float *tensor_scale, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The quantized weights of n_experts linears (descriptor only; device memory):
+ * expert e's codes, scales (MMA layout) and tensor scale follow those of
+ * e - 1, each as mxq_quantize writes an N x K weight (rows = N, cols = K). */
+typedef struct mxq_expert_weight {
+    int32_t fmt, n_experts;
+    int64_t rows, cols;
+    const void *codes;            /* n_experts * mxq_codes_bytes              */
+    const void *scales;           /* n_experts * mxq_scales_bytes; NULL for FP8_TENSOR */
+    const float *tensor_scales;   /* fp32[n_experts] (NVFP4, FP8_TENSOR)      */
+} mxq_expert_weight;
+
+/* Host only: bytes of codes and scales of such a weight. */
+mxq_status mxq_expert_weight_bytes(int32_t fmt, int32_t n_experts, int64_t rows, int64_t cols, size_t bytes[2]);
+
+/* Quantizes w (n_experts x N x K fp32/bf16 device) into the buffers of `out`
+ * (one mxq_quantize per expert; done once, when a model is loaded).
+ *   workspace: device scratch of mxq_quantize_workspace_bytes(fmt).
+ * Errors: as mxq_quantize; MXQ_EUNSUPPORTED (fmt). */
+mxq_status mxq_expert_weight_prepare(const void *w, int32_t wdtype, int32_t hadamard_b,
+                                     const mxq_expert_weight *out, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/* Products by expert, one kernel launch:
+ *   y[r] = deq(xq)[r] . deq(w of r's expert)^T,  r in [offsets[0], offsets[n_experts])
+ * on tcgen05 tensor cores, with the arithmetic of mxq_qlinear for each row.
+ * INT8_ROW is the product of 8-bit integers with a scale per token and per
+ * channel.  Other rows of y are left as they are.
+ *   xq: from mxq_quantize_grouped (layout MXQ_LAYOUT_MMA, rows = capacity),
+ *     fmt and cols those of w.
+ *   offsets: device int32[w->n_experts + 1], those xq was written with.
+ *   y: xq->rows x w->rows device, fp32 or bf16, 16-byte aligned.
+ * Constraints: K % 64 == 0 (4 bits) or K % 32 == 0 (8 bits); pointers 16-byte
+ * aligned.  Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED (format, format pair),
+ * MXQ_ECUDA; a pipeline wait that runs out is reported by mxq_check(). */
+mxq_status mxq_qlinear_grouped(const mxq_qtensor *xq, const int32_t *offsets, const mxq_expert_weight *w,
+                               void *y, int32_t ydtype, void *stream);
+
+/* Back to token order: out[t] = sum over i of weights[t][i] * y[slot[t][i]],
+ * added in fp32 (one FMA per term) in the order of i, dropped choices left
+ * out; a token without any gives zeros.
+ *   y: rows x n fp32/bf16 device; slot: device int32[tokens][topk]; weights:
+ *     device fp32[tokens][topk] or NULL (all 1).
+ *   out: tokens x n fp32/bf16 device, not overlapping y.
+ * A slot at or above rows is left out and reported by mxq_check() as
+ * MXQ_EINVAL.  Constraints: tokens * n < 2^31.
+ * Errors: MXQ_EINVAL, MXQ_ECUDA. */
+mxq_status mxq_expert_combine(const void *y, int32_t ydtype, int64_t rows, int64_t n, const int32_t *slot,
+                              const float *weights, int64_t tokens, int32_t topk, void *out, int32_t odtype,
+                              void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Query and key heads behind the q/k/v linear.                            */
+/* ---------------------------------------------------------------------- */
+
+typedef enum mxq_norm { MXQ_NORM_RMS = 0, MXQ_NORM_LAYER = 1 } mxq_norm;
+
+/* The heads of a step and how they are normed and turned.  Heads of a token
+ * lie one after the other; q_stride / k_stride elements lie between tokens,
+ * so q and k may be parts of a q/k/v row. */
+typedef struct mxq_heads {
+    const void *q, *k;             /* device, 16-byte aligned (NULL when it has no heads) */
+    int64_t q_stride, k_stride;    /* multiples of 8                          */
+    int32_t q_heads, k_heads;
+    int32_t head_dim;              /* multiple of 8, 8 .. 256                 */
+    int32_t dtype;                 /* mxq_dtype of q and k                    */
+    int64_t tokens;
+    int32_t norm;                  /* mxq_norm                                */
+    float eps;
+    const float *q_weight, *k_weight;   /* device fp32[head_dim] or NULL (all 1) */
+    int32_t rot_dim;               /* multiple of 8, 0 .. head_dim: the elements turned */
+    int32_t interleaved;           /* pairs (2i, 2i + 1), else (i, i + rot_dim / 2) */
+    const float *cos_table, *sin_table;  /* device fp32[n_positions][rot_dim / 2] */
+    int64_t n_positions;
+    const void *positions;         /* device integers[tokens], or NULL: token t has position t */
+    int32_t position_bits;         /* 32 or 64                                */
+} mxq_heads;
+
+/* Norm of every q and k head with the position rotation in the same pass:
+ *   v = x / sqrt(mean(x^2) + eps) * weight   (MXQ_NORM_LAYER: x - mean(x)
+ *   for x, the mean square of that), then for the pairs (a, b) of the first
+ *   rot_dim elements a' = a c - b s, b' = b c + a s with c, s of the token's
+ *   position and pair; fp32, rounded once (RNE) for bf16.
+ *   q_out, k_out: device, dtype of h, strides in elements as q and k; q_out
+ *     may be q (same stride), k_out may be k.
+ * A position outside [0, n_positions) makes its token's heads NaN and is
+ * reported by mxq_check() as MXQ_EINVAL.
+ * Errors: MXQ_EINVAL (shapes, strides, pointers, alignment), MXQ_ECUDA. */
+mxq_status mxq_qk_norm_rope(const mxq_heads *h, void *q_out, int64_t q_out_stride, void *k_out,
+                            int64_t k_out_stride, void *stream);
+
+/* The same, then the block-diagonal Hadamard rotation of size hadamard_b (0:
+ * none; a power of two dividing head_dim) and quantization of the fp32
+ * values, for a low-bit cache or product: codes and scales in the canonical
+ * layout of mxq_quantize, of a (tokens * heads) x head_dim matrix (row
+ * t * heads + head), which mxq_dequantize reads.
+ *   fmt: MXQ_MXFP8, MXQ_MXFP4 or MXQ_INT8_ROW (one scale per head); others
+ *     MXQ_EUNSUPPORTED.
+ * Constraints: head_dim % 32 == 0.  Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED,
+ * MXQ_ECUDA. */
+mxq_status mxq_qk_norm_rope_quantize(const mxq_heads *h, int32_t fmt, int32_t hadamard_b, void *q_codes,
+                                     void *q_scales, void *k_codes, void *k_scales, void *stream);
 
 #ifdef __cplusplus
 }

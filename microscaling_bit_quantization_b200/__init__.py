@@ -11,6 +11,7 @@ There is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -26,6 +27,7 @@ FORMATS = {"MXFP8": MXFP8, "MXFP4": MXFP4, "NVFP4": NVFP4, "INT4_G32": INT4_G32,
 FORMAT_NAMES = {v: k for k, v in FORMATS.items()}
 CANONICAL, MMA = 0, 1
 F32, BF16 = 0, 1
+NORMS = {"rms": 0, "layer": 1}
 STATUS = {0: "MXQ_OK", 1: "MXQ_EINVAL", 2: "MXQ_EUNSUPPORTED", 3: "MXQ_ECUDA", 4: "MXQ_ETIMEOUT", 5: "MXQ_ENOSPACE"}
 
 # Every entry point the header declares.
@@ -40,7 +42,10 @@ EXPORTS = ("mxq_status_string", "mxq_last_cuda_error_string", "mxq_device_suppor
            "mxq_qlinear_w4a16_workspace_bytes", "mxq_route",
            "mxq_quantize_lowrank_workspace_bytes", "mxq_quantize_lowrank", "mxq_quantize_lowrank_noalloc",
            "mxq_qlinear_routed_workspace_bytes", "mxq_qlinear_routed", "mxq_mixed_plan", "mxq_mixed_weight_bytes",
-           "mxq_mixed_prepare", "mxq_qlinear_mixed_workspace_bytes", "mxq_qlinear_mixed")
+           "mxq_mixed_prepare", "mxq_qlinear_mixed_workspace_bytes", "mxq_qlinear_mixed",
+           "mxq_expert_plan_workspace_bytes", "mxq_expert_plan", "mxq_grouped_scales_bytes", "mxq_quantize_grouped",
+           "mxq_expert_weight_bytes", "mxq_expert_weight_prepare", "mxq_qlinear_grouped", "mxq_expert_combine",
+           "mxq_qk_norm_rope", "mxq_qk_norm_rope_quantize")
 
 
 class MxqError(RuntimeError):
@@ -68,6 +73,22 @@ class _MixedC(ctypes.Structure):
                 ("choice", ctypes.c_void_p), ("group_index", ctypes.c_void_p), ("mx_codes", ctypes.c_void_p),
                 ("mx_scales", ctypes.c_void_p), ("i4_codes", ctypes.c_void_p), ("i4_scales", ctypes.c_void_p),
                 ("nv_values", ctypes.c_void_p), ("nv_tensor_scale", ctypes.c_void_p)]
+
+
+class _ExpertWeightC(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("tensor_scales", ctypes.c_void_p)]
+
+
+class _HeadsC(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("cos_table", ctypes.c_void_p), ("sin_table", ctypes.c_void_p), ("n_positions", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("position_bits", ctypes.c_int32)]
 
 
 def _load():
@@ -120,6 +141,16 @@ def _load():
         "mxq_qlinear_mixed": (i32, [ctypes.POINTER(_QTensorC), ctypes.POINTER(_MixedC), P, i32, P, sz, P]),
         "mxq_qlinear_routed": (i32, [P, i32, i64, i64, ctypes.POINTER(_LayerC), P, i32, i32, i32, i32, i32, P, i32,
                                      ctypes.POINTER(ctypes.c_int32), P, sz, P]),
+        "mxq_expert_plan_workspace_bytes": (i32, [i64, i32, psz]),
+        "mxq_expert_plan": (i32, [P, i32, i64, i32, P, P, P, sz, P]),
+        "mxq_grouped_scales_bytes": (i32, [i32, i64, i32, i64, psz]),
+        "mxq_quantize_grouped": (i32, [P, i32, i64, i64, i32, i32, P, i32, P, i32, i64, P, P, P, P, sz, P]),
+        "mxq_expert_weight_bytes": (i32, [i32, i32, i64, i64, psz]),
+        "mxq_expert_weight_prepare": (i32, [P, i32, i32, ctypes.POINTER(_ExpertWeightC), P, sz, P]),
+        "mxq_qlinear_grouped": (i32, [ctypes.POINTER(_QTensorC), P, ctypes.POINTER(_ExpertWeightC), P, i32, P]),
+        "mxq_expert_combine": (i32, [P, i32, i64, i64, P, P, i64, i32, P, i32, P]),
+        "mxq_qk_norm_rope": (i32, [ctypes.POINTER(_HeadsC), P, i64, P, i64, P]),
+        "mxq_qk_norm_rope_quantize": (i32, [ctypes.POINTER(_HeadsC), i32, i32, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -625,6 +656,294 @@ def qlinear_mixed(xq: QTensor, mw: MixedWeight, out_dtype=torch.bfloat16, out: t
     _ok(_lib.mxq_qlinear_mixed(ctypes.byref(xc), ctypes.byref(mc), _ptr(y), _dtype_code(y), _ptr(workspace),
                                workspace.numel(), _stream(stream)), "mxq_qlinear_mixed")
     return y
+
+
+# ---------------------------------------------------------------------------
+# Linears of a mixture of experts: rows in expert order.  These calls run on
+# the device of their tensors; with `stream` given, what they allocate belongs
+# to that stream.
+
+def _placed(f):
+    """Runs f with its first tensor's device, and `stream`, as the current ones."""
+    @functools.wraps(f)
+    def call(x, *args, stream=None, **kwargs):
+        dev = x.codes.device if isinstance(x, QTensor) else x.device
+        if dev.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device (there is no CPU path)")
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError("stream of %s for tensors of %s" % (stream.device, dev))
+            with torch.cuda.stream(stream):
+                return f(x, *args, **kwargs)
+        if dev.index != torch.cuda.current_device():
+            with torch.cuda.device(dev):
+                return f(x, *args, **kwargs)
+        return f(x, *args, **kwargs)
+    return call
+
+
+def _want(t: Optional[torch.Tensor], what: str, dtype, dev, shape=None, numel=None):
+    """The address of a contiguous device tensor, or None; raises on anything else."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+    if t.device != dev:
+        raise ValueError("%s is on %s, not %s" % (what, t.device, dev))
+    if not t.is_contiguous():
+        raise ValueError("%s has to be contiguous" % what)
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError("%s has shape %s, not %s" % (what, tuple(t.shape), shape))
+    if numel is not None and t.numel() < numel:
+        raise ValueError("%s has %d elements, fewer than %d" % (what, t.numel(), numel))
+    return t.data_ptr() if t.numel() else None
+
+
+def _raw_stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _plain_qtensor(q: QTensor, fmt: int, layout: int, rows: int, cols: int, scales_bytes_: int, dev, what: str):
+    """Checks a QTensor's sizes; returns its three addresses."""
+    if (q.fmt, q.layout, q.rows, q.cols) != (fmt, layout, rows, cols):
+        raise ValueError("%s: a %s tensor of %d x %d in layout %d is wanted" % (what, FORMAT_NAMES[fmt], rows, cols, layout))
+    for name, t, need in (("codes", q.codes, rows * cols // (2 if fmt in (MXFP4, NVFP4) else 1)),
+                          ("scales", q.scales, scales_bytes_), ("tensor_scale", q.tensor_scale,
+                                                                4 if fmt in (NVFP4, FP8_TENSOR) else 0)):
+        if need and (t is None or t.device != dev or not t.is_contiguous() or t.numel() * t.element_size() < need):
+            raise ValueError("%s.%s: %d contiguous bytes on %s are wanted" % (what, name, need, dev))
+    return _ptr(q.codes), _ptr(q.scales), _ptr(q.tensor_scale)
+
+
+@dataclass
+class ExpertPlan:
+    """Rows in expert order: expert e has rows offsets[e] .. offsets[e + 1] - 1;
+    slot[t, i] is the row of token t's i-th choice, -1 for a dropped one."""
+    offsets: torch.Tensor
+    slot: torch.Tensor
+
+
+def expert_plan_workspace_bytes(rows: int, n_experts: int) -> int:
+    return _size(_lib.mxq_expert_plan_workspace_bytes, rows, n_experts)
+
+
+@_placed
+def expert_plan(expert_ids: torch.Tensor, n_experts: int, out: ExpertPlan = None,
+                workspace: torch.Tensor = None) -> ExpertPlan:
+    """Plan of a routing: expert_ids int32/int64 [tokens, topk], ids outside [0, n_experts) dropped."""
+    if expert_ids.dtype not in (torch.int32, torch.int64) or expert_ids.dim() != 2:
+        raise TypeError("expert_ids: a 2-D int32 or int64 tensor is wanted")
+    ids, dev = expert_ids.contiguous(), expert_ids.device
+    rows = ids.numel()
+    if out is None:
+        out = ExpertPlan(torch.empty(n_experts + 1, dtype=torch.int32, device=dev),
+                         torch.empty(ids.shape, dtype=torch.int32, device=dev))
+    need = expert_plan_workspace_bytes(rows, n_experts)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _ok(_lib.mxq_expert_plan(_ptr(ids), 64 if ids.dtype == torch.int64 else 32, rows, n_experts,
+                             _want(out.offsets, "offsets", torch.int32, dev, (n_experts + 1,)),
+                             _want(out.slot, "slot", torch.int32, dev, tuple(ids.shape)),
+                             _want(workspace, "workspace", torch.uint8, dev) if need else None,
+                             workspace.numel() if need else 0, _raw_stream()), "mxq_expert_plan")
+    return out
+
+
+def grouped_scales_bytes(fmt: int, rows: int, n_groups: int, cols: int) -> int:
+    return _size(_lib.mxq_grouped_scales_bytes, fmt, rows, n_groups, cols)
+
+
+def alloc_grouped(fmt: int, rows: int, n_groups: int, cols: int, device="cuda") -> QTensor:
+    """Buffers of `rows` rows in expert order (layout MMA, scales in the grouped layout)."""
+    sb = grouped_scales_bytes(fmt, rows, n_groups, cols)
+    return QTensor(fmt, MMA, rows, cols, torch.empty(codes_bytes(fmt, rows, cols, MMA), dtype=torch.uint8, device=device),
+                   torch.empty(sb, dtype=torch.uint8, device=device) if sb else None,
+                   torch.empty(1, dtype=torch.float32, device=device) if fmt in (NVFP4, FP8_TENSOR) else None)
+
+
+@_placed
+def quantize_grouped(x: torch.Tensor, fmt: int, offsets: torch.Tensor, slot: torch.Tensor = None, hadamard_b: int = 0,
+                     out: QTensor = None, workspace: torch.Tensor = None) -> QTensor:
+    """Quantizes tokens x [tokens, cols] into expert order (slot int32
+    [tokens, topk]), or rows that are in expert order already (slot None)."""
+    dev = x.device
+    if x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x: a contiguous 2-D tensor is wanted")
+    tokens, cols = x.shape
+    n_groups = offsets.numel() - 1
+    topk = 1
+    if slot is not None:
+        if slot.dim() != 2 or slot.shape[0] != tokens:
+            raise ValueError("slot: int32 [%d, topk] is wanted" % tokens)
+        topk = slot.shape[1]
+    rows = out.rows if out is not None else tokens * topk
+    if out is None:
+        out = alloc_grouped(fmt, rows, n_groups, cols, dev)
+    codes, scales, ts = _plain_qtensor(out, fmt, MMA, rows, cols, grouped_scales_bytes(fmt, rows, n_groups, cols), dev, "out")
+    wsb = 0
+    if fmt in (NVFP4, FP8_TENSOR):
+        wsb = quantize_workspace_bytes(fmt)
+        if workspace is None:
+            workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
+    _ok(_lib.mxq_quantize_grouped(_ptr(x), _dtype_code(x), tokens, cols, fmt, hadamard_b,
+                                  _want(offsets, "offsets", torch.int32, dev), n_groups,
+                                  _want(slot, "slot", torch.int32, dev), topk, rows, codes, scales, ts,
+                                  _want(workspace, "workspace", torch.uint8, dev, numel=wsb) if wsb else None, wsb,
+                                  _raw_stream()), "mxq_quantize_grouped")
+    return out
+
+
+@dataclass
+class ExpertWeight:
+    """The quantized weights [rows, cols] of n_experts linears, one after the other (MMA layout)."""
+    fmt: int
+    n_experts: int
+    rows: int
+    cols: int
+    codes: torch.Tensor
+    scales: Optional[torch.Tensor]
+    tensor_scales: Optional[torch.Tensor]
+
+    def c(self) -> _ExpertWeightC:
+        return _ExpertWeightC(self.fmt, self.n_experts, self.rows, self.cols, _ptr(self.codes), _ptr(self.scales),
+                              _ptr(self.tensor_scales))
+
+
+def expert_weight_bytes(fmt: int, n_experts: int, rows: int, cols: int):
+    out = (ctypes.c_size_t * 2)()
+    _ok(_lib.mxq_expert_weight_bytes(fmt, n_experts, rows, cols, out), "mxq_expert_weight_bytes")
+    return out[0], out[1]
+
+
+@_placed
+def prepare_experts(w: torch.Tensor, fmt: int, hadamard_b: int = 0) -> ExpertWeight:
+    """Quantizes the weights w [experts, N, K] of a layer's experts once."""
+    if w.dim() != 3:
+        raise ValueError("w: [experts, N, K] is wanted")
+    w, dev = w.contiguous(), w.device
+    e, n, k = w.shape
+    cb, sb = expert_weight_bytes(fmt, e, n, k)
+    ew = ExpertWeight(fmt, e, n, k, torch.empty(cb, dtype=torch.uint8, device=dev),
+                      torch.empty(sb, dtype=torch.uint8, device=dev) if sb else None,
+                      torch.empty(e, dtype=torch.float32, device=dev) if fmt in (NVFP4, FP8_TENSOR) else None)
+    wsb = quantize_workspace_bytes(fmt)
+    ws = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
+    wc = ew.c()
+    _ok(_lib.mxq_expert_weight_prepare(_ptr(w), _dtype_code(w), hadamard_b, ctypes.byref(wc), _ptr(ws), wsb,
+                                       _raw_stream()), "mxq_expert_weight_prepare")
+    return ew
+
+
+@_placed
+def qlinear_grouped(xq: QTensor, w: ExpertWeight, offsets: torch.Tensor, out_dtype=torch.bfloat16,
+                    out: torch.Tensor = None) -> torch.Tensor:
+    """y[r] = deq(xq)[r] . deq(w[expert of row r])^T for the rows of every expert; other rows of `out` stay."""
+    dev = xq.codes.device
+    if out is None:
+        out = torch.empty((xq.rows, w.rows), dtype=out_dtype, device=dev)
+    xc, wc = xq.c(), w.c()
+    _ok(_lib.mxq_qlinear_grouped(ctypes.byref(xc), _want(offsets, "offsets", torch.int32, dev, (w.n_experts + 1,)),
+                                 ctypes.byref(wc), _want(out, "out", out.dtype, dev, (xq.rows, w.rows)),
+                                 _dtype_code(out), _raw_stream()), "mxq_qlinear_grouped")
+    return out
+
+
+@_placed
+def expert_combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = None, out_dtype=None,
+                   out: torch.Tensor = None) -> torch.Tensor:
+    """out[t] = sum_i weights[t, i] y[slot[t, i]] (weights None: 1; dropped choices left out)."""
+    dev = y.device
+    if y.dim() != 2 or slot.dim() != 2:
+        raise ValueError("y and slot: 2-D tensors are wanted")
+    rows, n = y.shape
+    tokens, topk = slot.shape
+    if out is None:
+        out = torch.empty((tokens, n), dtype=out_dtype or y.dtype, device=dev)
+    _ok(_lib.mxq_expert_combine(_want(y, "y", y.dtype, dev), _dtype_code(y), rows, n,
+                                _want(slot, "slot", torch.int32, dev),
+                                _want(weights, "weights", torch.float32, dev, (tokens, topk)), tokens, topk,
+                                _want(out, "out", out.dtype, dev, (tokens, n)), _dtype_code(out), _raw_stream()),
+        "mxq_expert_combine")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Query and key heads behind the q/k/v linear.
+
+def _token_stride(x: torch.Tensor, what: str) -> int:
+    """Elements between the tokens of [tokens, heads, dim] whose heads lie one after the other."""
+    t, h, d = x.shape
+    if d > 1 and x.stride(2) != 1 or h > 1 and x.stride(1) != d:
+        raise ValueError("%s: the heads of a token have to lie one after the other" % what)
+    return x.stride(0) if t > 1 else h * d
+
+
+def _heads(q, k, q_weight, k_weight, cos, sin, positions, eps, norm, interleaved) -> _HeadsC:
+    dev = q.device
+    if q.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or
+                                           k.dtype != q.dtype or k.device != dev)):
+        raise ValueError("q and k: [tokens, heads, head_dim] of one type and device are wanted")
+    tokens, hq, d = q.shape
+    n_pos, half = (0, 0) if cos is None else cos.shape
+    if cos is not None and (sin is None or sin.shape != cos.shape):
+        raise ValueError("sin: the shape of cos is wanted")
+    if positions is not None and positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions: int32 or int64 is wanted")
+    f32 = torch.float32
+    return _HeadsC(_ptr(q), _ptr(k), _token_stride(q, "q"), 0 if k is None else _token_stride(k, "k"), hq,
+                   0 if k is None else k.shape[1], d, _dtype_code(q), tokens, NORMS[norm], eps,
+                   _want(q_weight, "q_weight", f32, dev, (d,)), _want(k_weight, "k_weight", f32, dev, (d,)), 2 * half,
+                   int(interleaved), _want(cos, "cos", f32, dev), _want(sin, "sin", f32, dev), n_pos,
+                   None if positions is None else _want(positions, "positions", positions.dtype, dev, (tokens,)),
+                   64 if positions is not None and positions.dtype == torch.int64 else 32)
+
+
+@_placed
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor = None, q_weight: torch.Tensor = None, k_weight: torch.Tensor = None,
+                 cos: torch.Tensor = None, sin: torch.Tensor = None, positions: torch.Tensor = None, eps: float = 1e-6,
+                 norm: str = "rms", interleaved: bool = False, q_out: torch.Tensor = None, k_out: torch.Tensor = None):
+    """Norm of every head of q and k ([tokens, heads, head_dim], parts of a
+    q/k/v row allowed) and the rotation by its token's position (cos, sin:
+    fp32 [positions, rot_dim / 2]).  q_out may be q, k_out may be k.  Returns
+    (q_out, k_out)."""
+    h = _heads(q, k, q_weight, k_weight, cos, sin, positions, eps, norm, interleaved)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    for x, o, what in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if x is not None and (o.shape != x.shape or o.dtype != x.dtype or o.device != x.device):
+            raise ValueError("%s: %s %s on %s is wanted" % (what, x.dtype, tuple(x.shape), x.device))
+    _ok(_lib.mxq_qk_norm_rope(ctypes.byref(h), _ptr(q_out), _token_stride(q_out, "q_out"),
+                              _ptr(k_out) if k is not None else None,
+                              _token_stride(k_out, "k_out") if k is not None else 0, _raw_stream()), "mxq_qk_norm_rope")
+    return q_out, k_out
+
+
+@_placed
+def qk_norm_rope_quantize(q: torch.Tensor, k: torch.Tensor = None, q_weight: torch.Tensor = None,
+                          k_weight: torch.Tensor = None, cos: torch.Tensor = None, sin: torch.Tensor = None,
+                          positions: torch.Tensor = None, eps: float = 1e-6, norm: str = "rms",
+                          interleaved: bool = False, fmt: int = MXFP8, hadamard_b: int = 0, q_out: QTensor = None,
+                          k_out: QTensor = None):
+    """qk_norm_rope, then an optional Hadamard rotation of every head and its
+    codes in fmt (MXFP8, MXFP4, INT8_ROW; canonical layout, row
+    token * heads + head).  Returns (QTensor of q, QTensor of k)."""
+    h = _heads(q, k, q_weight, k_weight, cos, sin, positions, eps, norm, interleaved)
+    ptrs, res = [], []
+    for x, o, what in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if x is None:
+            ptrs += [None, None]
+            res.append(None)
+            continue
+        rows, d = x.shape[0] * x.shape[1], x.shape[2]
+        if o is None:
+            o = alloc_qtensor(fmt, rows, d, CANONICAL, x.device)
+        ptrs += _plain_qtensor(o, fmt, CANONICAL, rows, d, scales_bytes(fmt, rows, d), x.device, what)[:2]
+        res.append(o)
+    _ok(_lib.mxq_qk_norm_rope_quantize(ctypes.byref(h), fmt, hadamard_b, *ptrs, _raw_stream()),
+        "mxq_qk_norm_rope_quantize")
+    return tuple(res)
 
 
 def check(stream=None) -> int:

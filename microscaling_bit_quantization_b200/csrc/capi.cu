@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/mxq.h"
+#include "groups.cuh"
 #include "mxq_formats.cuh"
 #include "mxq_internal.h"
 
@@ -90,7 +91,8 @@ mxq_status mxq_check(void *stream) {
     unsigned int w = 0;
     e = read_and_clear_error(&w);
     if (e != cudaSuccess) return from_cuda(e);
-    return w ? MXQ_ETIMEOUT : MXQ_OK;
+    if (w & ~kErrIndex) return MXQ_ETIMEOUT;
+    return w ? MXQ_EINVAL : MXQ_OK;
 }
 
 mxq_status mxq_selftest_wait_timeout(uint32_t wait_us, void *stream) {
@@ -835,6 +837,263 @@ mxq_status mxq_qlinear_mixed(const mxq_qtensor *xq, const mxq_mixed_weight *w, v
     if (e == cudaSuccess && single < 0)
         e = launch_mixed_scatter(ybuf, w->n_group, w->choice, w->group_index, y, ybf, m, n, s);
     return from_cuda(e);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Rows in expert order, and the q/k head step.
+namespace {
+
+bool grouped_fmt(int32_t f) {   // formats whose GEMM applies the scales without a group epilogue
+    return f == MXQ_MXFP8 || f == MXQ_MXFP4 || f == MXQ_NVFP4 || f == MXQ_INT8_ROW || f == MXQ_FP8_TENSOR;
+}
+bool valid_groups(int64_t rows, int32_t n_groups) {
+    return rows >= 0 && rows <= kMaxGroupedRows && n_groups >= 1 && n_groups <= kMaxGroups;
+}
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+mxq_status mxq_expert_plan_workspace_bytes(int64_t rows, int32_t n_experts, size_t *bytes) {
+    if (!valid_groups(rows, n_experts) || !bytes) return MXQ_EINVAL;
+    *bytes = plan_workspace_bytes(rows, n_experts);
+    return MXQ_OK;
+}
+
+mxq_status mxq_expert_plan(const void *expert_ids, int32_t id_bits, int64_t rows, int32_t n_experts, int32_t *offsets,
+                           int32_t *slot, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!valid_groups(rows, n_experts) || (id_bits != 32 && id_bits != 64) || !offsets || !aligned4(offsets))
+        return MXQ_EINVAL;
+    if (rows > 0 && (!expert_ids || !slot || !aligned4(slot) ||
+                     (reinterpret_cast<uintptr_t>(expert_ids) & (uintptr_t)(id_bits / 8 - 1)) != 0))
+        return MXQ_EINVAL;
+    const size_t need = plan_workspace_bytes(rows, n_experts);
+    if (need && (!workspace || !aligned4(workspace))) return MXQ_EINVAL;
+    if (workspace_bytes < need) return MXQ_ENOSPACE;
+    return from_cuda(launch_expert_plan(expert_ids, id_bits == 64, rows, n_experts, offsets, slot, (int32_t *)workspace,
+                                        (cudaStream_t)stream));
+}
+
+mxq_status mxq_grouped_scales_bytes(int32_t fmt, int64_t rows, int32_t n_groups, int64_t cols, size_t *bytes) {
+    if (!valid_fmt(fmt) || !valid_groups(rows, n_groups) || !bytes || !valid_shape(fmt, rows, cols)) return MXQ_EINVAL;
+    if (!grouped_fmt(fmt)) return MXQ_EUNSUPPORTED;
+    if (fmt_byte_scales(fmt))
+        *bytes = (size_t)(grouped_scale_tiles(rows, n_groups) * 128 * round_up(cols / fmt_block(fmt), 16));
+    else
+        *bytes = fmt == MXQ_INT8_ROW ? (size_t)(rows * 4) : 0;
+    return MXQ_OK;
+}
+
+mxq_status mxq_quantize_grouped(const void *x, int32_t xdtype, int64_t x_rows, int64_t cols, int32_t fmt,
+                                int32_t hadamard_b, const int32_t *offsets, int32_t n_groups, const int32_t *slot,
+                                int32_t topk, int64_t rows, void *codes, void *scales, float *tensor_scale,
+                                void *workspace, size_t workspace_bytes, void *stream) {
+    if (!valid_fmt(fmt) || !valid_dtype(xdtype) || !valid_shape(fmt, x_rows, cols) || !valid_shape(fmt, rows, cols) ||
+        cols <= 0 || !valid_hadamard(hadamard_b, cols) || !valid_groups(rows, n_groups))
+        return MXQ_EINVAL;
+    if (!grouped_fmt(fmt)) return MXQ_EUNSUPPORTED;
+    if (!offsets || !aligned4(offsets) || !aligned4(slot) || topk < 1 || topk > 32 ||
+        (!slot && x_rows > 0 && (topk != 1 || x_rows > rows)))
+        return MXQ_EINVAL;
+    const bool ts = fmt_tensor_scaled(fmt);
+    if (ts && (!tensor_scale || !workspace || !aligned4(workspace))) return MXQ_EINVAL;
+    if (ts && workspace_bytes < kLrHeader) return MXQ_ENOSPACE;
+    if (x_rows > 0 && (!x || !aligned16(x))) return MXQ_EINVAL;
+    if (rows > 0 && (!codes || !aligned16(codes) || (fmt != MXQ_FP8_TENSOR && (!scales || !aligned4(scales)))))
+        return MXQ_EINVAL;
+    if (!ts && (x_rows == 0 || rows == 0)) return MXQ_OK;
+    return from_cuda(launch_quantize_grouped(x, xdtype == MXQ_BF16, x_rows, cols, fmt, hadamard_b, offsets, n_groups, slot,
+                                             topk, rows, codes, scales, tensor_scale, (float *)workspace,
+                                             (cudaStream_t)stream));
+}
+
+mxq_status mxq_expert_weight_bytes(int32_t fmt, int32_t n_experts, int64_t rows, int64_t cols, size_t bytes[2]) {
+    if (!bytes || n_experts < 1 || n_experts > kMaxGroups) return MXQ_EINVAL;
+    if (valid_fmt(fmt) && !grouped_fmt(fmt)) return MXQ_EUNSUPPORTED;
+    size_t c = 0, sc = 0;
+    mxq_status st = mxq_codes_bytes(fmt, rows, cols, MXQ_LAYOUT_MMA, &c);
+    if (st == MXQ_OK) st = mxq_scales_bytes(fmt, rows, cols, MXQ_LAYOUT_MMA, &sc);
+    if (st != MXQ_OK) return st;
+    bytes[0] = c * (size_t)n_experts;
+    bytes[1] = sc * (size_t)n_experts;
+    return MXQ_OK;
+}
+
+// Shape rules of a grouped weight (as mxq_qlinear's for each expert).
+static mxq_status check_expert_weight(const mxq_expert_weight *w) {
+    if (!w || !valid_fmt(w->fmt) || w->n_experts < 1 || w->n_experts > kMaxGroups) return MXQ_EINVAL;
+    if (!grouped_fmt(w->fmt)) return MXQ_EUNSUPPORTED;
+    if (w->rows < 0 || w->cols <= 0 || w->cols % (fmt_is4(w->fmt) ? 64 : 32) || !valid_shape(w->fmt, w->rows, w->cols))
+        return MXQ_EINVAL;
+    // the kernels index the experts' rows and scale atoms together in 31 bits
+    const int64_t tiles = (w->rows + 127) / 128;
+    if (w->n_experts * (tiles + 1) * 128 >= ((int64_t)1 << 31) ||
+        w->n_experts * tiles * (round_up(w->cols / 16, 16) / 4) >= ((int64_t)1 << 31))
+        return MXQ_EINVAL;
+    if (w->rows > 0) {
+        if (!w->codes || !aligned16(w->codes)) return MXQ_EINVAL;
+        if (w->fmt != MXQ_FP8_TENSOR && (!w->scales || !aligned16(w->scales))) return MXQ_EINVAL;
+        if (fmt_tensor_scaled(w->fmt) && (!w->tensor_scales || !aligned4(w->tensor_scales))) return MXQ_EINVAL;
+    }
+    return MXQ_OK;
+}
+
+mxq_status mxq_expert_weight_prepare(const void *w, int32_t wdtype, int32_t hadamard_b, const mxq_expert_weight *out,
+                                     void *workspace, size_t workspace_bytes, void *stream) {
+    const mxq_status st = check_expert_weight(out);
+    if (st != MXQ_OK) return st;
+    if (!valid_dtype(wdtype) || !valid_hadamard(hadamard_b, out->cols)) return MXQ_EINVAL;
+    if (out->rows > 0 && (!w || !aligned16(w))) return MXQ_EINVAL;
+    size_t cb = 0, sb = 0;
+    mxq_codes_bytes(out->fmt, out->rows, out->cols, MXQ_LAYOUT_MMA, &cb);
+    mxq_scales_bytes(out->fmt, out->rows, out->cols, MXQ_LAYOUT_MMA, &sb);
+    const size_t elems = (size_t)(out->rows * out->cols) * (wdtype == MXQ_BF16 ? 2 : 4);
+    for (int32_t e = 0; e < out->n_experts && out->rows > 0; e++) {
+        float *ts = fmt_tensor_scaled(out->fmt) ? const_cast<float *>(out->tensor_scales) + e : nullptr;
+        void *sc = sb ? (char *)const_cast<void *>(out->scales) + sb * (size_t)e : nullptr;
+        const mxq_status q = mxq_quantize((const char *)w + elems * (size_t)e, wdtype, out->rows, out->cols, out->fmt,
+                                          hadamard_b, MXQ_LAYOUT_MMA, (char *)const_cast<void *>(out->codes) + cb * (size_t)e,
+                                          sc, ts, workspace, workspace_bytes, stream);
+        if (q != MXQ_OK) return q;
+    }
+    return MXQ_OK;
+}
+
+mxq_status mxq_qlinear_grouped(const mxq_qtensor *xq, const int32_t *offsets, const mxq_expert_weight *w, void *y,
+                               int32_t ydtype, void *stream) {
+    if (!xq || !valid_fmt(xq->fmt) || !valid_dtype(ydtype)) return MXQ_EINVAL;
+    const mxq_status st = check_expert_weight(w);
+    if (st != MXQ_OK) return st;
+    if (xq->fmt != w->fmt) return MXQ_EUNSUPPORTED;
+    if (xq->layout != MXQ_LAYOUT_MMA || xq->cols != w->cols || !valid_groups(xq->rows, w->n_experts) ||
+        !valid_shape(xq->fmt, xq->rows, xq->cols) || !offsets || !aligned4(offsets))
+        return MXQ_EINVAL;
+    const int64_t m = xq->rows, n = w->rows, k = w->cols;
+    const int64_t tiles = grouped_scale_tiles(m, w->n_experts);
+    // items, their K stages and X's scale atoms are counted in 31 bits
+    if (tiles * ((n + 127) / 128) * (k / 16) >= ((int64_t)1 << 31) || tiles * (round_up(k / 16, 16) / 4) >= ((int64_t)1 << 31))
+        return MXQ_EINVAL;
+    if (m == 0 || n == 0) return MXQ_OK;
+    if (!y || !aligned16(y) || !xq->codes || !aligned16(xq->codes)) return MXQ_EINVAL;
+    if (xq->fmt != MXQ_FP8_TENSOR && (!xq->scales || !aligned16(xq->scales))) return MXQ_EINVAL;
+    if (fmt_tensor_scaled(xq->fmt) && (!xq->tensor_scale || !aligned4(xq->tensor_scale))) return MXQ_EINVAL;
+    GroupedOperands op;
+    memset(&op, 0, sizeof(op));
+    op.fmt = w->fmt;
+    op.rows = m;
+    op.n = n;
+    op.k = k;
+    op.n_groups = w->n_experts;
+    op.offsets = offsets;
+    op.x_codes = xq->codes;
+    op.x_scales = xq->scales;
+    op.w_codes = w->codes;
+    op.w_scales = w->scales;
+    op.x_tensor_scale = xq->tensor_scale;
+    op.w_tensor_scales = w->tensor_scales;
+    op.y = y;
+    op.y_bf16 = ydtype == MXQ_BF16;
+    return from_cuda(launch_qlinear_grouped(op, (cudaStream_t)stream));
+}
+
+mxq_status mxq_expert_combine(const void *y, int32_t ydtype, int64_t rows, int64_t n, const int32_t *slot,
+                              const float *weights, int64_t tokens, int32_t topk, void *out, int32_t odtype,
+                              void *stream) {
+    if (!valid_dtype(ydtype) || !valid_dtype(odtype) || rows < 0 || rows > kMaxGroupedRows || n < 0 || tokens < 0 ||
+        topk < 1 || topk > 32 || n >= ((int64_t)1 << 31) || tokens >= ((int64_t)1 << 31) || (n > 0 && tokens >= ((int64_t)1 << 31) / n))
+        return MXQ_EINVAL;
+    if (tokens == 0 || n == 0) return MXQ_OK;
+    if (!slot || !aligned4(slot) || !aligned4(weights) || !out || (rows > 0 && !y)) return MXQ_EINVAL;
+    const uintptr_t ya = ydtype == MXQ_BF16 ? 1 : 3, oa = odtype == MXQ_BF16 ? 1 : 3;
+    if ((reinterpret_cast<uintptr_t>(y) & ya) || (reinterpret_cast<uintptr_t>(out) & oa)) return MXQ_EINVAL;
+    return from_cuda(launch_expert_combine(y, ydtype == MXQ_BF16, rows, n, slot, weights, tokens, topk, out,
+                                           odtype == MXQ_BF16, (cudaStream_t)stream));
+}
+
+// Arguments that both forms of the head step share.
+static mxq_status check_heads(const mxq_heads *h, HeadArgs *a) {
+    if (!h || !valid_dtype(h->dtype) || h->tokens < 0 || h->q_heads < 0 || h->k_heads < 0 || h->q_heads > 65536 ||
+        h->k_heads > 65536 || h->head_dim < 8 || h->head_dim > 256 || h->head_dim % 8 || h->rot_dim < 0 ||
+        h->rot_dim > h->head_dim || h->rot_dim % 8 || (h->norm != MXQ_NORM_RMS && h->norm != MXQ_NORM_LAYER) ||
+        !(h->eps >= 0.0f))
+        return MXQ_EINVAL;
+    if (h->tokens > ((int64_t)1 << 40)) return MXQ_EINVAL;
+    if (h->positions && h->position_bits != 32 && h->position_bits != 64) return MXQ_EINVAL;
+    if (h->positions && (reinterpret_cast<uintptr_t>(h->positions) & (uintptr_t)(h->position_bits / 8 - 1))) return MXQ_EINVAL;
+    if (h->rot_dim > 0 && h->tokens > 0) {
+        if (!h->cos_table || !h->sin_table || !aligned16(h->cos_table) || !aligned16(h->sin_table) || h->n_positions < 1)
+            return MXQ_EINVAL;
+        if (!h->positions && h->tokens > h->n_positions) return MXQ_EINVAL;
+    }
+    const bool q = h->q_heads > 0 && h->tokens > 0, k = h->k_heads > 0 && h->tokens > 0;
+    if (q && (!h->q || !aligned16(h->q) || h->q_stride % 8 || h->q_stride < (int64_t)h->q_heads * h->head_dim)) return MXQ_EINVAL;
+    if (k && (!h->k || !aligned16(h->k) || h->k_stride % 8 || h->k_stride < (int64_t)h->k_heads * h->head_dim)) return MXQ_EINVAL;
+    if (!aligned16(h->q_weight) || !aligned16(h->k_weight)) return MXQ_EINVAL;
+    memset(a, 0, sizeof(*a));
+    a->q = h->q;
+    a->k = h->k;
+    a->q_stride = h->q_stride;
+    a->k_stride = h->k_stride;
+    a->q_heads = h->q_heads;
+    a->k_heads = h->k_heads;
+    a->head_dim = h->head_dim;
+    a->rot = h->rot_dim;
+    a->interleaved = h->interleaved != 0;
+    a->norm = h->norm;
+    a->tokens = h->tokens;
+    a->n_pos = h->n_positions;
+    a->q_weight = h->q_weight;
+    a->k_weight = h->k_weight;
+    a->eps = h->eps;
+    a->cos_t = h->cos_table;
+    a->sin_t = h->sin_table;
+    a->positions = h->positions;
+    a->pos64 = h->position_bits == 64;
+    a->bf16 = h->dtype == MXQ_BF16;
+    a->fmt = -1;
+    return MXQ_OK;
+}
+
+mxq_status mxq_qk_norm_rope(const mxq_heads *h, void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                            void *stream) {
+    HeadArgs a;
+    const mxq_status st = check_heads(h, &a);
+    if (st != MXQ_OK) return st;
+    const bool q = h->q_heads > 0 && h->tokens > 0, k = h->k_heads > 0 && h->tokens > 0;
+    if (q && (!q_out || !aligned16(q_out) || q_out_stride % 8 || q_out_stride < (int64_t)h->q_heads * h->head_dim))
+        return MXQ_EINVAL;
+    if (k && (!k_out || !aligned16(k_out) || k_out_stride % 8 || k_out_stride < (int64_t)h->k_heads * h->head_dim))
+        return MXQ_EINVAL;
+    if (!q && !k) return MXQ_OK;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    return from_cuda(launch_qk_norm_rope(a, (cudaStream_t)stream));
+}
+
+mxq_status mxq_qk_norm_rope_quantize(const mxq_heads *h, int32_t fmt, int32_t hadamard_b, void *q_codes, void *q_scales,
+                                     void *k_codes, void *k_scales, void *stream) {
+    HeadArgs a;
+    const mxq_status st = check_heads(h, &a);
+    if (st != MXQ_OK) return st;
+    if (!valid_fmt(fmt)) return MXQ_EINVAL;
+    if (fmt != MXQ_MXFP8 && fmt != MXQ_MXFP4 && fmt != MXQ_INT8_ROW) return MXQ_EUNSUPPORTED;
+    if (h->head_dim % 32 || !valid_hadamard(hadamard_b, h->head_dim)) return MXQ_EINVAL;
+    const bool q = h->q_heads > 0 && h->tokens > 0, k = h->k_heads > 0 && h->tokens > 0;
+    if (q && (!q_codes || !q_scales || !aligned16(q_codes) || !aligned4(q_scales))) return MXQ_EINVAL;
+    if (k && (!k_codes || !k_scales || !aligned16(k_codes) || !aligned4(k_scales))) return MXQ_EINVAL;
+    if (!q && !k) return MXQ_OK;
+    a.fmt = fmt;
+    a.hadamard_b = hadamard_b;
+    a.q_out = q_codes;
+    a.k_out = k_codes;
+    a.q_scales = q_scales;
+    a.k_scales = k_scales;
+    return from_cuda(launch_qk_norm_rope(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,664 @@
+// experts.cu -- the steps on either side of a grouped product by expert
+// (mixture-of-experts linears in the library's formats): the plan that gives
+// every (token, choice) its row in expert order, the quantizer that writes
+// tokens into that order, and the weighted sum that brings the products back
+// to token order.
+//
+// Expert order: the rows of expert e are [offsets[e], offsets[e + 1]), the
+// choices of one expert in token order.  slot[t][i] is the row of token t's
+// i-th choice, negative for a dropped one.
+#include <cuda_runtime.h>
+
+#include "groups.cuh"
+#include "mxq_formats.cuh"
+#include "mxq_internal.h"
+#include "tc_ptx.cuh"
+
+namespace mxq {
+namespace {
+
+// ------------------------------------------------------------------ plan
+//
+// A stable counting sort without moving any data: slot = offsets[e] + the
+// number of earlier choices of e.  A block counts its choices per warp in
+// shared memory, turns the counts into starting rows (scan over experts, then
+// over the block's warps), and walks its choices again: the choices of one
+// expert among 32 consecutive ones are ranked by __match_any_sync, the
+// warp's counter carries the rank on.  No atomic decides an order, so the
+// plan is the same from run to run.  Up to kPlanOneBlock choices one block
+// does it all (one launch); above that a first kernel writes each block's
+// counts, and every block of the second sums those of the blocks before it.
+// Bound: latency, both memory passes being a few MB.
+
+constexpr int kPlanThreads = 512;   // >= kMaxGroups: a thread per expert in the scan
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanOneBlock = 4096;
+constexpr int kPlanBlockRows = 2048;
+static_assert(kPlanThreads >= kMaxGroups, "one thread per expert");
+
+template <typename I>
+__device__ __forceinline__ int expert_at(const I *ids, int64_t i, int64_t end, int n) {
+    if (i >= end) return -1;
+    const I v = ids[i];
+    return v >= 0 && v < (I)n ? (int)v : -1;
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kPlanThreads) k_plan_count(const I *__restrict__ ids, int64_t rows, int n,
+                                                             int64_t per_block, int32_t *__restrict__ counts) {
+    __shared__ int hist[kMaxGroups];
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int e = threadIdx.x; e < n; e += kPlanThreads) hist[e] = 0;
+    __syncthreads();
+    const int64_t begin = (int64_t)blockIdx.x * per_block;
+    const int64_t end = begin + per_block < rows ? begin + per_block : rows;
+    for (int64_t i0 = begin + threadIdx.x; i0 < end; i0 += 4 * kPlanThreads) {
+        int e[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) e[j] = expert_at(ids, i0 + j * kPlanThreads, end, n);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (e[j] >= 0) atomicAdd(hist + e[j], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < n; e += kPlanThreads) counts[(int64_t)blockIdx.x * n + e] = hist[e];
+}
+
+// counts: null with one block, else k_plan_count's.
+template <typename I>
+__global__ void __launch_bounds__(kPlanThreads)
+    k_plan_place(const I *__restrict__ ids, int64_t rows, int n, int64_t per_block, const int32_t *__restrict__ counts,
+                 int32_t *__restrict__ offsets, int32_t *__restrict__ slot) {
+    __shared__ int at[kPlanWarps][kMaxGroups];   // counts, then the next row, of each warp's choices of each expert
+    __shared__ int warp_sum[kPlanWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int i = threadIdx.x; i < kPlanWarps * kMaxGroups; i += kPlanThreads) (&at[0][0])[i] = 0;
+    __syncthreads();
+    const int64_t begin = (int64_t)blockIdx.x * per_block;
+    const int64_t end = begin + per_block < rows ? begin + per_block : rows;
+    // contiguous choices per warp, whole groups of 32
+    const int64_t per_warp = ((end - begin + kPlanThreads - 1) / kPlanThreads) * 32;
+    const int64_t w_begin = begin + warp * per_warp;
+    const int64_t w_end = w_begin + per_warp < end ? w_begin + per_warp : end;
+    for (int64_t i0 = w_begin; i0 < w_end; i0 += 128) {
+        int e[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) e[j] = expert_at(ids, i0 + 32 * j + lane, w_end, n);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (e[j] >= 0) atomicAdd(&at[warp][e[j]], 1);   // a count: no order in it
+    }
+    __syncthreads();
+    int own = 0, before = 0, total = 0;
+    const int e = threadIdx.x;
+    if (e < n) {
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; w++) own += at[w][e];
+        total = own;
+        if (counts) {
+            total = 0;
+#pragma unroll 8
+            for (int b = 0; b < (int)gridDim.x; b++) {
+                const int c = counts[(int64_t)b * n + e];
+                if (b == (int)blockIdx.x) before = total;
+                total += c;
+            }
+        }
+    }
+    // exclusive scan of the totals over the experts
+    int scan = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    int first = scan - total;
+    for (int w = 0; w < warp; w++) first += warp_sum[w];
+    if (e < n) {
+        if (blockIdx.x == 0) {
+            offsets[e] = first;
+            if (e == n - 1) offsets[n] = first + total;
+        }
+        int next = first + before;
+#pragma unroll
+        for (int w = 0; w < kPlanWarps; w++) {
+            const int c = at[w][e];
+            at[w][e] = next;
+            next += c;
+        }
+    }
+    __syncthreads();
+    const unsigned below = (1u << lane) - 1u, above = ~(below | (1u << lane));
+    for (int64_t i0 = w_begin; i0 < w_end; i0 += 128) {
+        int ex[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) ex[j] = expert_at(ids, i0 + 32 * j + lane, w_end, n);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const unsigned same = __match_any_sync(0xFFFFFFFFu, ex[j]);
+            int r = -1;
+            if (ex[j] >= 0) r = at[warp][ex[j]] + __popc(same & below);
+            __syncwarp();
+            if (ex[j] >= 0 && !(same & above)) at[warp][ex[j]] = r + 1;   // the last of them carries the rank on
+            __syncwarp();
+            const int64_t i = i0 + 32 * j + lane;
+            if (i < w_end) slot[i] = r;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ quantize in expert order
+//
+// A token is read and coded once and its codes written to the rows of all
+// its choices: T K reads and T k K writes, against k times the reads of a
+// gather.  A warp takes 32 consecutive 16-element chunks of a token (the
+// chunk mapping of k_quantize, so blocks and Hadamard blocks lie in aligned
+// lanes), and lane i looks up choice i's row and its place in the grouped
+// scale layout while the chunk's load is in flight.  Four block scales are
+// gathered into the 4-byte word they share in a scale atom.
+// Bound: HBM.
+
+constexpr int kGqThreads = 256;
+constexpr int kGqWarps = kGqThreads / 32;
+constexpr int kGqMaxCtas = 960;   // per-CTA maxima of the tensor-amax pass
+
+struct GroupedQuantArgs {
+    int64_t x_rows, cols, rows;   // rows: capacity of codes and scales
+    FastDiv segs;                 // warps' worth of chunks per token
+    uint32_t n_segs, units;       // units = x_rows * n_segs
+    const int32_t *slot;          // null: token t is row t
+    int topk;
+    const int32_t *offsets;
+    int n_groups;
+    int hadamard_b;
+    uint32_t s_pad4, scale_tiles;   // padded scale columns / 4, 128-row tiles the scales buffer holds
+    uint8_t *codes;
+    uint8_t *scales;
+    float *tensor_scale;
+    float *amax_slots;
+    int n_slots;
+    unsigned int *err;
+};
+
+// Row of choice `lane` of token t (lanes below topk; -1 elsewhere and for
+// rows outside the groups).
+__device__ __forceinline__ int choice_row(const GroupedQuantArgs &a, uint32_t t, int lane, int first, int last) {
+    int r = -1;
+    if (lane < a.topk) {
+        r = a.slot ? a.slot[(int64_t)t * a.topk + lane] : (int)t;
+        if (r < first || r >= last) r = -1;
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_or_zero(const T *p, bool valid, float v[16]) {
+    if (valid) load16(p, v);
+    else {
+#pragma unroll
+        for (int i = 0; i < 16; i++) v[i] = 0.0f;
+    }
+}
+
+__device__ __forceinline__ void unpack16(const uint4 (&k)[2], float (&v)[16]) {   // bf16
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint32_t w[4] = {k[i].x, k[i].y, k[i].z, k[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+            v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    }
+}
+__device__ __forceinline__ void unpack16(const uint4 (&k)[4], float (&v)[16]) {   // fp32
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        v[4 * i] = __uint_as_float(k[i].x);
+        v[4 * i + 1] = __uint_as_float(k[i].y);
+        v[4 * i + 2] = __uint_as_float(k[i].z);
+        v[4 * i + 3] = __uint_as_float(k[i].w);
+    }
+}
+
+// max |x| over the tokens that have a row, one maximum per CTA.
+template <typename T>
+__global__ void __launch_bounds__(kGqThreads) k_amax_grouped(const T *__restrict__ x, GroupedQuantArgs a) {
+    __shared__ float wm[kGqWarps];
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int first = clamp_row(a.offsets[0], a.rows), last = clamp_row(a.offsets[a.n_groups], a.rows);
+    const float norm = a.hadamard_b ? __frsqrt_rn((float)a.hadamard_b) : 1.0f;
+    const uint32_t cpr = (uint32_t)(a.cols >> 4);
+    float m = 0.0f;
+    for (uint32_t u = blockIdx.x * kGqWarps + (threadIdx.x >> 5); u < a.units; u += gridDim.x * kGqWarps) {
+        const uint32_t t = fdiv(u, a.segs), c = (u - t * a.n_segs) * 32 + lane;
+        float v[16];
+        load_or_zero(x + (int64_t)t * a.cols + (int64_t)c * 16, c < cpr, v);
+        const int r = choice_row(a, t, lane, first, last);
+        if (!__any_sync(0xFFFFFFFFu, r >= 0)) continue;
+        if (a.hadamard_b) hadamard_chunk_n(v, a.hadamard_b, lane, norm);
+        m = fmaxf(m, amax16(v));
+    }
+    m = group_max<32>(m);
+    if (lane == 0) wm[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < kGqWarps; w++) m = fmaxf(m, wm[w]);
+        a.amax_slots[blockIdx.x] = m;
+    }
+}
+
+// Formats with byte scales, and FP8 per tensor.
+template <typename T, int F>
+__global__ void __launch_bounds__(kGqThreads) k_quantize_grouped(const T *__restrict__ x, GroupedQuantArgs a) {
+    __shared__ Groups groups;
+    __shared__ float wm[kGqWarps];
+    const int lane = threadIdx.x & 31;
+    constexpr bool kByte = fmt_byte_scales(F);
+    pdl_wait();
+    pdl_launch_dependents();
+    load_groups(groups, a.offsets, a.n_groups, a.rows, blockIdx.x == 0 ? a.err : nullptr);
+    const int first = groups.off[0], last = groups.off[a.n_groups];
+    const uint32_t cpr = (uint32_t)(a.cols >> 4);
+    TensorRecip tr;
+    Recip rt;
+    if (fmt_tensor_scaled(F)) {
+        float m = 0.0f;
+        for (int i = threadIdx.x; i < a.n_slots; i += kGqThreads) m = fmaxf(m, a.amax_slots[i]);
+        m = group_max<32>(m);
+        if (lane == 0) wm[threadIdx.x >> 5] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kGqWarps; w++) m = fmaxf(m, wm[w]);
+        const float s = F == kNVFP4 ? nvfp4_tensor_scale(m) : fp8_tensor_scale(m);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.tensor_scale = s;
+        if (F == kNVFP4) tr = tensor_recip_of(s);
+        else rt = recip_of(s);
+    }
+    const float norm = a.hadamard_b ? __frsqrt_rn((float)a.hadamard_b) : 1.0f;
+    for (uint32_t u = blockIdx.x * kGqWarps + (threadIdx.x >> 5); u < a.units; u += gridDim.x * kGqWarps) {
+        const uint32_t t = fdiv(u, a.segs), c = (u - t * a.n_segs) * 32 + lane;
+        const bool valid = c < cpr;
+        float v[16];
+        load_or_zero(x + (int64_t)t * a.cols + (int64_t)c * 16, valid, v);
+        int r = choice_row(a, t, lane, first, last);
+        uint32_t sr = 0;
+        if (kByte && r >= 0) {   // the row's place among the scales: its group's first tile, then its rank in the group
+            const int g = group_of_row(groups, a.n_groups, r);
+            if (g >= 0) sr = (uint32_t)(128 * groups.tile[g] + r - groups.off[g]);
+            if (g < 0 || (sr >> 7) >= a.scale_tiles) r = -1;   // offsets that do not fit the buffers
+        }
+        const unsigned any = __ballot_sync(0xFFFFFFFFu, r >= 0);
+        if (!any) continue;
+        if (a.hadamard_b) hadamard_chunk_n(v, a.hadamard_b, lane, norm);
+        uint32_t w[4];        // codes: 16 bytes (8-bit elements) or 8
+        uint32_t scale = 0;   // this lane's block scale
+        float amax = amax16(v);
+        if (F == kMXFP8 || F == kMXFP4) {
+            amax = group_max<2>(amax);
+            const bool zero = !(amax > 0.0f);
+            float inv = 0.0f, q[16];
+            scale = zero ? 127u : mx_scale(amax, F == kMXFP8 ? 8 : 2, inv);
+            mul8(v, inv, q);   // a power of two: exact
+            mul8(v + 8, inv, q + 8);
+            if (F == kMXFP8) {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    w[i] = zero ? 0u : cvt_e4m3x4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    w[i] = zero ? 0u : cvt_e2m1x8(q[8 * i], q[8 * i + 1], q[8 * i + 2], q[8 * i + 3], q[8 * i + 4],
+                                                  q[8 * i + 5], q[8 * i + 6], q[8 * i + 7]);
+            }
+        } else if (F == kNVFP4) {
+            float d;
+            scale = nvfp4_block_scale_fast(amax, tr, d);
+            w[0] = w[1] = 0u;
+            if (scale) {
+                const Recip rd = recip_of(d);
+                w[0] = e2m1x8_quot(v, rd);
+                w[1] = e2m1x8_quot(v + 8, rd);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) w[i] = e4m3x4_quot(v + 4 * i, rt);
+        }
+        uint32_t word = 0, col = 0;   // the four scales of an atom's 4-byte word, held by its first lane
+        bool leader = false;
+        if (kByte) {
+            constexpr int L = F == kNVFP4 ? 1 : 2;   // lanes per block
+            if (!valid) scale = 0u;
+            word = scale | (__shfl_down_sync(0xFFFFFFFFu, scale, L) << 8) |
+                   (__shfl_down_sync(0xFFFFFFFFu, scale, 2 * L) << 16) |
+                   (__shfl_down_sync(0xFFFFFFFFu, scale, 3 * L) << 24);
+            leader = valid && (lane & (4 * L - 1)) == 0;
+            col = c / L;
+        }
+        for (unsigned left = any; left; left &= left - 1) {
+            const int i = __ffs(left) - 1;
+            const int row = __shfl_sync(0xFFFFFFFFu, r, i);
+            const uint32_t srow = kByte ? __shfl_sync(0xFFFFFFFFu, sr, i) : 0u;
+            const int64_t chunk = (int64_t)row * cpr + c;
+            if (valid) {
+                if (fmt_is4(F)) *reinterpret_cast<uint2 *>(a.codes + chunk * 8) = make_uint2(w[0], w[1]);
+                else *reinterpret_cast<uint4 *>(a.codes + chunk * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (kByte && leader)
+                *reinterpret_cast<uint32_t *>(a.scales + mma_scale_offset(srow, col, (int64_t)a.s_pad4 * 4)) = word;
+        }
+    }
+}
+
+// INT8 per row: a warp per token; the first 8 chunks of a lane (rows up to
+// 4096 elements) stay in registers between the row maximum and the codes.
+template <typename T>
+__global__ void __launch_bounds__(kGqThreads) k_quantize_grouped_int8(const T *__restrict__ x, GroupedQuantArgs a) {
+    constexpr int kKeep = sizeof(T) == 2 ? 8 : 4;
+    constexpr int kWords = sizeof(T) * 16 / 16;
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int first = clamp_row(a.offsets[0], a.rows), last = clamp_row(a.offsets[a.n_groups], a.rows);
+    const float norm = a.hadamard_b ? __frsqrt_rn((float)a.hadamard_b) : 1.0f;
+    const uint32_t cpr = (uint32_t)(a.cols >> 4), steps = (cpr + 31) / 32;
+    for (uint32_t t = blockIdx.x * kGqWarps + (threadIdx.x >> 5); t < (uint32_t)a.x_rows; t += gridDim.x * kGqWarps) {
+        const T *xr = x + (int64_t)t * a.cols;
+        uint4 keep[kKeep][kWords];
+#pragma unroll
+        for (int j = 0; j < kKeep; j++) {
+            const uint32_t c = j * 32 + lane;
+#pragma unroll
+            for (int q = 0; q < kWords; q++)
+                keep[j][q] = c < cpr ? __ldg(reinterpret_cast<const uint4 *>(xr + (int64_t)c * 16) + q) : make_uint4(0, 0, 0, 0);
+        }
+        const int r = choice_row(a, t, lane, first, last);
+        const unsigned any = __ballot_sync(0xFFFFFFFFu, r >= 0);
+        if (!any) continue;
+        auto values = [&](uint32_t j, float (&v)[16]) {   // chunk j * 32 + lane, rotated
+            const uint32_t c = j * 32 + lane;
+            load_or_zero(xr + (int64_t)c * 16, c < cpr, v);
+            if (a.hadamard_b) hadamard_chunk_n(v, a.hadamard_b, lane, norm);
+        };
+        auto kept = [&](const uint4 (&k)[kWords], float (&v)[16]) {
+            unpack16(k, v);
+            if (a.hadamard_b) hadamard_chunk_n(v, a.hadamard_b, lane, norm);
+        };
+        float m = 0.0f, v[16];
+#pragma unroll
+        for (int j = 0; j < kKeep; j++)
+            if ((uint32_t)j < steps) {
+                kept(keep[j], v);
+                m = fmaxf(m, amax16(v));
+            }
+        for (uint32_t j = kKeep; j < steps; j++) {
+            values(j, v);
+            m = fmaxf(m, amax16(v));
+        }
+        m = group_max<32>(m);
+        const float s = __fdiv_rn(m, 127.0f);
+        const Recip rs = recip_of(s);
+        auto store = [&](uint32_t j, const float (&u)[16]) {
+            const uint32_t c = j * 32 + lane;
+            const uint4 w = make_uint4(int_x4_quot(u, rs, 127), int_x4_quot(u + 4, rs, 127), int_x4_quot(u + 8, rs, 127),
+                                       int_x4_quot(u + 12, rs, 127));
+            for (unsigned left = any; left; left &= left - 1) {
+                const int row = __shfl_sync(0xFFFFFFFFu, r, __ffs(left) - 1);
+                if (c < cpr) *reinterpret_cast<uint4 *>(a.codes + ((int64_t)row * cpr + c) * 16) = w;
+            }
+        };
+#pragma unroll
+        for (int j = 0; j < kKeep; j++)
+            if ((uint32_t)j < steps) {
+                kept(keep[j], v);
+                store(j, v);
+            }
+        for (uint32_t j = kKeep; j < steps; j++) {
+            values(j, v);
+            store(j, v);
+        }
+        if (r >= 0) reinterpret_cast<float *>(a.scales)[r] = s;
+    }
+}
+
+// ------------------------------------------------------------------ combine
+//
+// out[t] = sum over i of weights[t][i] y[slot[t][i]], fp32 FMAs in the order
+// of i.  A thread owns 8 columns of a token and has the rows of four choices
+// in flight at a time.  Bound: HBM.
+
+struct CombineArgs {
+    int64_t rows, n, total;   // total: threads' worth of work
+    FastDiv per_row;          // vectors per token
+    uint32_t n_vec;
+    const int32_t *slot;
+    const float *weights;
+    int topk;
+    unsigned int *err;
+};
+
+template <typename T, int V>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16, 8> {
+    uint4 q;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { q = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    }
+};
+template <>
+struct Vec<float, 8> {
+    float4 q[2];
+    __device__ __forceinline__ void load(const float *p) {
+        q[0] = __ldg(reinterpret_cast<const float4 *>(p));
+        q[1] = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            v[4 * j] = q[j].x;
+            v[4 * j + 1] = q[j].y;
+            v[4 * j + 2] = q[j].z;
+            v[4 * j + 3] = q[j].w;
+        }
+    }
+};
+template <typename T>
+struct Vec<T, 1> {
+    T q;
+    __device__ __forceinline__ void load(const T *p) { q = __ldg(p); }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = (float)q; }
+};
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&v)[8]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                               pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void store_vec(float *p, const float (&v)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&v)[1]) { *p = __float2bfloat16_rn(v[0]); }
+__device__ __forceinline__ void store_vec(float *p, const float (&v)[1]) { *p = v[0]; }
+
+template <typename T, typename O, int V>
+__global__ void __launch_bounds__(256) k_expert_combine(const T *__restrict__ y, O *__restrict__ out, CombineArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < a.total; u += (int64_t)gridDim.x * 256) {
+        const uint32_t t = fdiv((uint32_t)u, a.per_row), c = ((uint32_t)u - t * a.n_vec) * V;
+        float acc[V] = {};
+        for (int i0 = 0; i0 < a.topk; i0 += 4) {
+            Vec<T, V> q[4];
+            float w[4];
+            bool on[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int i = i0 + j;
+                const int r = i < a.topk ? a.slot[(int64_t)t * a.topk + i] : -1;
+                on[j] = r >= 0 && r < a.rows;
+                if (r >= a.rows) latch_index_error(a.err);
+                w[j] = 1.0f;
+                if (on[j]) {
+                    if (a.weights) w[j] = a.weights[(int64_t)t * a.topk + i];
+                    q[j].load(y + (int64_t)r * a.n + c);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (on[j]) {
+                    float v[V];
+                    q[j].get(v);
+#pragma unroll
+                    for (int k = 0; k < V; k++) acc[k] = __fmaf_rn(w[j], v[k], acc[k]);
+                }
+        }
+        store_vec(out + (int64_t)t * a.n + c, acc);
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*k)(KArgs...), int64_t grid, int threads, cudaStream_t s, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+// Blocks of the plan's kernels: one up to kPlanOneBlock choices, else enough
+// for kPlanBlockRows each, one per SM at most (every block of the second
+// kernel reads all counts).
+int plan_blocks(int64_t rows) {
+    if (rows <= kPlanOneBlock) return 1;
+    const int64_t b = (rows + kPlanBlockRows - 1) / kPlanBlockRows;
+    return (int)(b < kPlanMaxBlocks ? b : kPlanMaxBlocks);
+}
+
+template <typename I>
+cudaError_t plan(const I *ids, int64_t rows, int n, int32_t *offsets, int32_t *slot, int32_t *counts, cudaStream_t s) {
+    const int nb = plan_blocks(rows);
+    const int64_t per = (rows + nb - 1) / nb;
+    if (nb > 1) {
+        const cudaError_t e = launch_pdl(k_plan_count<I>, nb, kPlanThreads, s, ids, rows, n, per, counts);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(k_plan_place<I>, nb, kPlanThreads, s, ids, rows, n, per, (const int32_t *)(nb > 1 ? counts : nullptr),
+                      offsets, slot);
+}
+
+template <typename T>
+cudaError_t quantize_grouped(const T *x, int fmt, GroupedQuantArgs a, cudaStream_t s) {
+    const int64_t warps = fmt == kINT8Row ? a.x_rows : (int64_t)a.units;
+    int64_t ctas = (warps + kGqWarps - 1) / kGqWarps;
+    const int64_t cap = (int64_t)sm_count() * 8;
+    if (ctas > cap) ctas = cap;
+    if (ctas < 1) ctas = 1;   // no tokens: the tensor scale is still written
+    if (fmt == kINT8Row) return launch_pdl(k_quantize_grouped_int8<T>, ctas, kGqThreads, s, x, a);
+    if (fmt_tensor_scaled(fmt)) {
+        a.n_slots = (int)(ctas < kGqMaxCtas ? ctas : kGqMaxCtas);
+        const cudaError_t e = launch_pdl(k_amax_grouped<T>, a.n_slots, kGqThreads, s, x, a);
+        if (e != cudaSuccess) return e;
+    }
+    switch (fmt) {
+    case kMXFP8: return launch_pdl(k_quantize_grouped<T, kMXFP8>, ctas, kGqThreads, s, x, a);
+    case kMXFP4: return launch_pdl(k_quantize_grouped<T, kMXFP4>, ctas, kGqThreads, s, x, a);
+    case kNVFP4: return launch_pdl(k_quantize_grouped<T, kNVFP4>, ctas, kGqThreads, s, x, a);
+    default: return launch_pdl(k_quantize_grouped<T, kFP8Tensor>, ctas, kGqThreads, s, x, a);
+    }
+}
+
+template <typename T, typename O, int V>
+cudaError_t combine(const void *y, void *out, const CombineArgs &a, cudaStream_t s) {
+    int64_t ctas = (a.total + 255) / 256;
+    const int64_t cap = (int64_t)sm_count() * 64;
+    if (ctas > cap) ctas = cap;
+    return launch_pdl(k_expert_combine<T, O, V>, ctas, 256, s, (const T *)y, (O *)out, a);
+}
+
+}  // namespace
+
+size_t plan_workspace_bytes(int64_t rows, int n_experts) {
+    const int nb = plan_blocks(rows);
+    return nb > 1 ? (size_t)nb * n_experts * 4 : 0;
+}
+
+cudaError_t launch_expert_plan(const void *ids, bool ids64, int64_t rows, int n_experts, int32_t *offsets, int32_t *slot,
+                               int32_t *counts, cudaStream_t s) {
+    return ids64 ? plan((const int64_t *)ids, rows, n_experts, offsets, slot, counts, s)
+                 : plan((const int32_t *)ids, rows, n_experts, offsets, slot, counts, s);
+}
+
+cudaError_t launch_quantize_grouped(const void *x, bool bf16, int64_t x_rows, int64_t cols, int fmt, int hadamard_b,
+                                    const int32_t *offsets, int n_groups, const int32_t *slot, int topk, int64_t rows,
+                                    void *codes, void *scales, float *tensor_scale, float *amax_slots, cudaStream_t s) {
+    GroupedQuantArgs a = {};
+    const int64_t segs = (cols / 16 + 31) / 32;
+    a.x_rows = x_rows;
+    a.cols = cols;
+    a.rows = rows;
+    a.segs = make_fastdiv((uint32_t)segs);
+    a.n_segs = (uint32_t)segs;
+    a.units = (uint32_t)(x_rows * segs);
+    a.slot = slot;
+    a.topk = topk;
+    a.offsets = offsets;
+    a.n_groups = n_groups;
+    a.hadamard_b = hadamard_b;
+    const int blk = fmt_block(fmt);
+    if (fmt_byte_scales(fmt)) a.s_pad4 = (uint32_t)((cols / blk + 15) / 16 * 4);
+    a.scale_tiles = (uint32_t)grouped_scale_tiles(rows, n_groups);
+    a.codes = (uint8_t *)codes;
+    a.scales = (uint8_t *)scales;
+    a.tensor_scale = tensor_scale;
+    a.amax_slots = amax_slots;
+    const cudaError_t e = error_word_address(&a.err);
+    if (e != cudaSuccess) return e;
+    return bf16 ? quantize_grouped((const __nv_bfloat16 *)x, fmt, a, s) : quantize_grouped((const float *)x, fmt, a, s);
+}
+
+cudaError_t launch_expert_combine(const void *y, bool y_bf16, int64_t rows, int64_t n, const int32_t *slot,
+                                  const float *weights, int64_t tokens, int topk, void *out, bool out_bf16,
+                                  cudaStream_t s) {
+    CombineArgs a = {};
+    // 8 columns a thread where every row starts on a 16-byte boundary, else one
+    const bool vec = n % 8 == 0 && ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+    const int64_t per_row = vec ? n / 8 : n;
+    a.rows = rows;
+    a.n = n;
+    a.total = tokens * per_row;
+    a.per_row = make_fastdiv((uint32_t)per_row);
+    a.n_vec = (uint32_t)per_row;
+    a.slot = slot;
+    a.weights = weights;
+    a.topk = topk;
+    const cudaError_t e = error_word_address(&a.err);
+    if (e != cudaSuccess) return e;
+    using bf = __nv_bfloat16;
+    if (y_bf16) {
+        if (out_bf16) return vec ? combine<bf, bf, 8>(y, out, a, s) : combine<bf, bf, 1>(y, out, a, s);
+        return vec ? combine<bf, float, 8>(y, out, a, s) : combine<bf, float, 1>(y, out, a, s);
+    }
+    if (out_bf16) return vec ? combine<float, bf, 8>(y, out, a, s) : combine<float, bf, 1>(y, out, a, s);
+    return vec ? combine<float, float, 8>(y, out, a, s) : combine<float, float, 1>(y, out, a, s);
+}
+
+}  // namespace mxq

@@ -1,0 +1,73 @@
+// groups.cuh -- rows in expert order: the group table that the grouped
+// quantizer and the grouped products build from the device offsets, and the
+// bounds they hold those offsets to.
+#pragma once
+
+#include <stdint.h>
+
+#include "mxq_internal.h"
+
+namespace mxq {
+namespace {
+
+constexpr unsigned int kErrIndex = 256u;   // error word: an index in device data outside its range (mxq_check: MXQ_EINVAL)
+
+__device__ __forceinline__ void latch_index_error(unsigned int *err) {
+    if (err) atomicOr(err, kErrIndex);
+}
+
+// Offsets are device data the host cannot check: each is held to
+// [0, rows], and a group whose end lies before its start is empty, so that
+// no offset leads outside the buffers.
+__device__ __forceinline__ int clamp_row(int o, int64_t rows) {
+    return o < 0 ? 0 : (int64_t)o > rows ? (int)rows : o;
+}
+
+struct Groups {
+    int off[kMaxGroups + 1];
+    int tile[kMaxGroups + 1];   // 128-row scale tiles before each group
+};
+
+// Fills `g` (all threads of the block call this); a table that had to be
+// clamped is reported to *err when err is given.
+__device__ __forceinline__ void load_groups(Groups &g, const int32_t *offsets, int n, int64_t rows, unsigned int *err) {
+    for (int i = threadIdx.x; i <= n; i += blockDim.x) {
+        const int o = offsets[i];
+        g.off[i] = clamp_row(o, rows);
+        if (o != g.off[i] || (i > 0 && offsets[i - 1] > o)) latch_index_error(err);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int carry = 0;
+        for (int b = 0; b < n; b += 32) {
+            const int e = b + lane;
+            const int rows_e = e < n ? g.off[e + 1] - g.off[e] : 0;
+            const int t = rows_e > 0 ? (rows_e + 127) >> 7 : 0;
+            int s = t;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, s, o);
+                if (lane >= o) s += v;
+            }
+            if (e < n) g.tile[e] = carry + s - t;
+            carry += __shfl_sync(0xFFFFFFFFu, s, 31);
+        }
+        if (lane == 0) g.tile[n] = carry;
+    }
+    __syncthreads();
+}
+
+// The group that holds row r, or -1.
+__device__ __forceinline__ int group_of_row(const Groups &g, int n, int r) {
+    int lo = 0, hi = n;   // the last group that starts at or before r
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (g.off[mid] <= r) lo = mid;
+        else hi = mid;
+    }
+    return r >= g.off[lo] && r < g.off[lo + 1] ? lo : -1;
+}
+
+}  // namespace
+}  // namespace mxq

@@ -196,6 +196,62 @@ cudaError_t launch_mixed_scatter(const void *const ybuf[3], const int64_t n_grou
                                  const int32_t *group_index, void *y, bool y_bf16, int64_t m, int64_t n,
                                  cudaStream_t s);
 
+// ---- rows in expert order (experts.cu, gemm_grouped.cu, gemm.cu)
+// Groups (experts) of a grouped call, and rows in expert order: the wide
+// product kernel keeps a 16-bit count of 128-row tiles per group in the
+// shared memory its ring leaves, and rows / 128 + groups must fit it.
+constexpr int kMaxGroups = 512;
+constexpr int64_t kMaxGroupedRows = (int64_t)1 << 22;
+constexpr int kPlanMaxBlocks = 128;
+// 128-row tiles that the rows of n_groups groups can need: every group begins
+// a tile of its own.
+inline int64_t grouped_scale_tiles(int64_t rows, int64_t n_groups) {
+    return rows / 128 + (rows < n_groups ? rows : n_groups);
+}
+size_t plan_workspace_bytes(int64_t rows, int n_experts);
+cudaError_t launch_expert_plan(const void *ids, bool ids64, int64_t rows, int n_experts, int32_t *offsets, int32_t *slot,
+                               int32_t *counts, cudaStream_t s);
+// Tokens into expert order (slot null: token t is row t); rows: capacity of
+// codes and scales.  amax_slots: room for 960 floats (tensor-scaled formats).
+cudaError_t launch_quantize_grouped(const void *x, bool bf16, int64_t x_rows, int64_t cols, int fmt, int hadamard_b,
+                                    const int32_t *offsets, int n_groups, const int32_t *slot, int topk, int64_t rows,
+                                    void *codes, void *scales, float *tensor_scale, float *amax_slots, cudaStream_t s);
+cudaError_t launch_expert_combine(const void *y, bool y_bf16, int64_t rows, int64_t n, const int32_t *slot,
+                                  const float *weights, int64_t tokens, int topk, void *out, bool out_bf16,
+                                  cudaStream_t s);
+struct GroupedOperands {
+    int fmt;
+    int64_t rows, n, k;                     // rows: capacity of X and y in expert order
+    int n_groups;
+    const int32_t *offsets;
+    const void *x_codes, *x_scales;         // byte scales in the grouped MMA layout, or fp32 per row (INT8)
+    const void *w_codes, *w_scales;         // experts one after the other; byte scales in the MMA layout of each
+    const float *x_tensor_scale, *w_tensor_scales;
+    void *y;
+    bool y_bf16;
+};
+cudaError_t launch_qlinear_grouped(const GroupedOperands &op, cudaStream_t s);        // gemm_grouped.cu: the choice
+cudaError_t launch_qlinear_grouped_many(const GroupedOperands &op, cudaStream_t s);   // gemm.cu
+// q/k head norm and position rotation (heads.cu); fmt < 0: outputs in the
+// input's type, else codes and scales in that format.
+struct HeadArgs {
+    const void *q, *k;
+    int64_t q_stride, k_stride;             // elements between tokens
+    int q_heads, k_heads, head_dim, rot, interleaved, norm;
+    int64_t tokens, n_pos;
+    const float *q_weight, *k_weight;
+    float eps;
+    const float *cos_t, *sin_t;
+    const void *positions;                  // null: token t has position t
+    bool pos64;
+    void *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+    int fmt, hadamard_b;
+    void *q_scales, *k_scales;
+    bool bf16;
+};
+cudaError_t launch_qk_norm_rope(const HeadArgs &h, cudaStream_t s);
+
 // Device error word (bounded waits that ran out); read-and-clear, and its
 // device address on the current device (for kernels of other files).
 cudaError_t read_and_clear_error(unsigned int *value);

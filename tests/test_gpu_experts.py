@@ -1,0 +1,436 @@
+"""GPU parity of the calls that run a mixture of experts' linears: the plan,
+the quantizer into expert order, the products by expert and the sum back to
+token order.
+
+References: the plan against a stable argsort; codes and scales against the
+oracle's quantizer, bit for bit; products against the binary64 product of the
+oracle's dequantized operands with the tolerance of gpu_util.gemm_close
+(products exact in the tensor core, fp32 sums); the sum against binary64, the
+bound counting its fp32 roundings (topk FMAs, each off by at most 2^-24 of the
+partial sum, which no term sum of magnitudes is below) and the final one."""
+import numpy as np
+import pytest
+import torch
+
+import workloads
+from gpu_util import dev, gemm_close, host_values, mma_offset, nasty_matrix
+
+pytestmark = pytest.mark.gpu
+
+MXFP8, MXFP4, NVFP4, INT8_ROW, FP8_TENSOR = 0, 1, 2, 5, 6
+FMTS = (MXFP8, MXFP4, NVFP4, INT8_ROW, FP8_TENSOR)
+BLOCK = {MXFP8: 32, MXFP4: 32, NVFP4: 16}
+
+
+@pytest.fixture(scope="module")
+def mxq():
+    import microscaling_bit_quantization_b200 as m
+    assert torch.cuda.is_available() and m.lib().mxq_device_supported(0) == 1
+    m.check()
+    return m
+
+
+# ------------------------------------------------------------------ plan
+
+def ref_plan(ids, n):
+    flat = ids.reshape(-1)
+    ok = (flat >= 0) & (flat < n)
+    key = np.where(ok, flat, n)
+    order = np.argsort(key, kind="stable")
+    place = np.empty(flat.size, np.int64)
+    place[order] = np.arange(flat.size)
+    counts = np.bincount(key.astype(np.int64), minlength=n + 1)[:n]
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    return offsets.astype(np.int32), np.where(ok, place, -1).astype(np.int32).reshape(ids.shape)
+
+
+def check_plan(mxq, ids, n, dtype):
+    plan = mxq.expert_plan(torch.from_numpy(ids).to(dtype).cuda(), n)
+    off, slot = ref_plan(ids, n)
+    np.testing.assert_array_equal(plan.offsets.cpu().numpy(), off)
+    np.testing.assert_array_equal(plan.slot.cpu().numpy(), slot)
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+@pytest.mark.parametrize("tokens,topk,n", [(0, 4, 8), (1, 1, 1), (1, 8, 64), (5, 3, 512), (31, 1, 2), (33, 2, 33),
+                                           (512, 8, 128), (513, 8, 128), (4097, 1, 7), (2049, 3, 512), (40000, 8, 256),
+                                           (70001, 1, 3)])
+def test_plan(mxq, tokens, topk, n, dtype):
+    rng = np.random.default_rng(tokens + n)
+    ids = rng.integers(0, n, (tokens, topk))
+    check_plan(mxq, ids, n, dtype)
+    ids[rng.random((tokens, topk)) < 0.2] = -1
+    ids[rng.random((tokens, topk)) < 0.05] = n            # no such expert
+    check_plan(mxq, ids, n, dtype)
+
+
+def test_plan_one_expert_none_and_far_ids(mxq):
+    check_plan(mxq, np.full((3000, 2), 5), 9, torch.int32)
+    check_plan(mxq, np.full((9000, 2), 5), 9, torch.int64)
+    check_plan(mxq, np.full((9000, 2), -1), 9, torch.int32)
+    far = np.array([[2 ** 32, 1], [2 ** 40 + 3, -2 ** 33], [0, 2 ** 31]])
+    check_plan(mxq, far, 4, torch.int64)                  # ids whose low 32 bits name an expert
+
+
+# ------------------------------------------------------------------ quantize into expert order
+
+def routing(rng, tokens, topk, n, drop=0.1):
+    ids = np.stack([rng.permutation(n)[:topk] for _ in range(tokens)]) if tokens else np.zeros((0, topk), np.int64)
+    ids[rng.random(ids.shape) < drop] = -1
+    return ids
+
+
+def scale_rows(off, rows):
+    """Grouped scale row of every row in expert order, by walking the groups."""
+    out, tile = np.zeros(rows, np.int64), 0
+    for lo, hi in zip(off[:-1], off[1:]):
+        out[lo:hi] = 128 * tile + np.arange(hi - lo)
+        tile += (hi - lo + 127) // 128
+    return out
+
+
+def check_grouped(q, oq, fmt, off, src, fill):
+    """Rows of q in expert order against rows src of the oracle's oq; everything else still `fill`."""
+    used = int(off[-1])
+    codes = q.codes.cpu().numpy().reshape(q.rows, -1)
+    np.testing.assert_array_equal(codes[:used], oq.codes.view(np.uint8).reshape(oq.rows, -1)[src])
+    assert (codes[used:] == fill).all()
+    if fmt in BLOCK:
+        sp = (q.cols // BLOCK[fmt] + 15) // 16 * 16
+        buf = q.scales.cpu().numpy()
+        at = mma_offset(scale_rows(off, q.rows)[:used, None], np.arange(q.cols // BLOCK[fmt])[None], sp)
+        np.testing.assert_array_equal(buf[at], oq.scales[src])
+    elif fmt == INT8_ROW:
+        s = q.scales.cpu().view(torch.float32).numpy()
+        np.testing.assert_array_equal(s[:used].view(np.uint32), oq.scales[src].view(np.uint32))
+        assert (q.scales.cpu().numpy().reshape(-1, 4)[used:] == fill).all()
+    if fmt in (NVFP4, FP8_TENSOR):
+        np.testing.assert_array_equal(np.float32(q.tensor_scale.item()), np.float32(oq.tensor_scale))
+
+
+def filled(mxq, fmt, rows, groups, cols, fill=0xFF):
+    q = mxq.alloc_grouped(fmt, rows, groups, cols)
+    q.codes.fill_(fill)
+    if q.scales is not None:
+        q.scales.fill_(fill)
+    return q
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("tokens,topk,n,cols,had,dtype", [
+    (37, 3, 5, 64, 0, "bf16"), (1, 8, 64, 1152, 32, "f32"), (150, 1, 2, 576, 0, "f32"), (300, 4, 7, 4608, 0, "bf16"),
+    (64, 2, 300, 192, 64, "bf16"), (9, 2, 3, 5120, 256, "bf16"), (33, 32, 40, 64, 16, "f32")])
+def test_quantize_grouped(mxq, orc, fmt, tokens, topk, n, cols, had, dtype):
+    rng = np.random.default_rng(tokens * 7 + fmt)
+    x = nasty_matrix(fmt + tokens, tokens, cols)
+    ids = routing(rng, tokens, topk, n)
+    ids[0, 0] = 1
+    if tokens > 8:
+        ids[7] = -1                                       # a padded token: its values reach nothing
+    off, slot = ref_plan(ids, n)
+    placed = (slot >= 0).any(1)
+    vals = host_values(x, dtype)
+    xd = dev(x, dtype)
+    xd[torch.from_numpy(~placed).cuda()] = float("nan")
+    q = filled(mxq, fmt, tokens * topk, n, cols)
+    out = mxq.quantize_grouped(xd, fmt, torch.from_numpy(off).cuda(), torch.from_numpy(slot).cuda(), had, out=q)
+    assert out is q and mxq.check() == 0
+    src = np.zeros(int(off[-1]), np.int64)
+    compact = np.cumsum(placed) - 1                       # row among the placed tokens
+    for t, i in zip(*np.nonzero(slot >= 0)):
+        src[slot[t, i]] = compact[t]
+    # every bit as mxq_quantize writes it, for the tokens that have a row
+    lib = mxq.quantize(dev(vals[placed], dtype), fmt, had)
+    sc = None if lib.scales is None else lib.scales.cpu().numpy()
+    oq = orc.quantize(vals[placed], fmt, had)
+    same = Bits(lib.codes.cpu().numpy().reshape(oq.rows, -1),
+                sc.reshape(oq.rows, -1) if fmt in BLOCK else None if sc is None else sc.view(np.float32),
+                None if lib.tensor_scale is None else lib.tensor_scale.item(), oq.rows)
+    check_grouped(q, same, fmt, off, src, 0xFF)
+    # and as the oracle has them.  The matrix holds blocks of values near 3e38: 32 of them added by a rotation of 64
+    # or 256 pass the largest fp32 value (3.4e38), and the definition, fp32 butterflies, then gives infinities and
+    # their differences, NaN, whose maximum the definition does not name; such rows have no oracle value
+    finite = np.ones(oq.rows, bool)
+    if had:
+        with np.errstate(over="ignore", invalid="ignore"):
+            finite = np.isfinite(orc.hadamard(vals[placed], had)).all(1)
+    if finite.all():
+        check_grouped(q, oq, fmt, off, src, 0xFF)
+    elif fmt not in (NVFP4, FP8_TENSOR):                  # there one such row decides the scale of all
+        for a, b in ((same.codes, oq.codes.view(np.uint8).reshape(oq.rows, -1)), (same.scales, oq.scales)):
+            np.testing.assert_array_equal(a[finite], b[finite])
+
+
+class Bits:
+    def __init__(self, codes, scales, tensor_scale, rows):
+        self.codes, self.scales, self.tensor_scale, self.rows = codes, scales, tensor_scale, rows
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantize_rows_in_order_and_empty(mxq, orc, fmt):
+    rng = np.random.default_rng(fmt)
+    off = np.array([0, 0, 130, 131, 131, 200], np.int32)
+    x = rng.standard_normal((230, 256)).astype(np.float32)
+    xd = dev(x, "bf16")
+    xd[200:] = float("nan")                               # rows behind the last group
+    q = filled(mxq, fmt, 230, 5, 256)
+    mxq.quantize_grouped(xd, fmt, torch.from_numpy(off).cuda(), out=q)
+    assert mxq.check() == 0
+    check_grouped(q, orc.quantize(host_values(x, "bf16")[:200], fmt), fmt, off, np.arange(200), 0xFF)
+    none = filled(mxq, fmt, 6, 3, 64)
+    zero = torch.zeros(4, dtype=torch.int32, device="cuda")
+    mxq.quantize_grouped(xd[:3, :64].contiguous(), fmt, zero, torch.full((3, 2), -1, dtype=torch.int32, device="cuda"), out=none)
+    assert mxq.check() == 0 and (none.codes == 0xFF).all()
+    if fmt in (NVFP4, FP8_TENSOR):
+        assert none.tensor_scale.item() == 1.0
+    mxq.quantize_grouped(xd[:0], fmt, zero, torch.zeros((0, 2), dtype=torch.int32, device="cuda"))
+    assert mxq.check() == 0
+
+
+# ------------------------------------------------------------------ products
+
+def deq64(q):
+    return np.asarray(q.dequantize(), np.float64)
+
+
+class Experts:
+    """Expert weights and rows in expert order, with the binary64 product."""
+
+    def __init__(self, mxq, orc, fmt, counts, n, k, extra=0, seed=0, had=0):
+        rng = np.random.default_rng(seed + fmt)
+        self.counts, e = counts, len(counts)
+        self.off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        rows = int(self.off[-1]) + extra
+        x = rng.standard_t(4, (rows, k)).astype(np.float32)
+        x[:, rng.choice(k, max(1, k // 64), replace=False)] *= 30
+        x = workloads.to_bf16_values(x)
+        w = workloads.to_bf16_values((rng.standard_normal((e, n, k)) * 0.02).astype(np.float32))
+        self.w = mxq.prepare_experts(dev(w, "bf16"), fmt, had)
+        self.offsets = torch.from_numpy(self.off).cuda()
+        self.xq = filled(mxq, fmt, rows, e, k)            # scales nobody writes: NaN in every byte format
+        xd = dev(x, "bf16")
+        xd[int(self.off[-1]):] = float("nan")
+        mxq.quantize_grouped(xd, fmt, self.offsets, hadamard_b=had, out=self.xq)
+        used = int(self.off[-1])
+        self.ref = np.zeros((used, n))
+        self.owq = [orc.quantize(w[i], fmt, had) for i in range(e)]
+        if used:
+            xv = deq64(orc.quantize(x[:used], fmt, had))
+            for i in range(e):
+                lo, hi = self.off[i], self.off[i + 1]
+                self.ref[lo:hi] = xv[lo:hi] @ deq64(self.owq[i]).T
+
+    def run(self, mxq, out_dtype):
+        y = torch.full((self.xq.rows, self.w.rows), 7.0, dtype=out_dtype, device="cuda")
+        mxq.qlinear_grouped(self.xq, self.w, self.offsets, out=y)
+        assert mxq.check() == 0
+        return y
+
+    def check(self, mxq, out_dtype):
+        y = self.run(mxq, out_dtype)
+        used = int(self.off[-1])
+        assert (y[used:] == 7.0).all()                    # rows behind the last group stay
+        if used:
+            gemm_close(y[:used].float().cpu().numpy(), self.ref, bf16_out=out_dtype == torch.bfloat16)
+        return y
+
+
+FEW = [([1], 128, 128), ([0, 3, 0, 1, 0], 264, 512), ([17, 128, 129, 0, 40, 1], 100, 320), ([64, 5], 520, 1152),
+       ([2, 0, 1, 1, 0, 4, 1, 1], 2048, 4096), ([33, 31, 32, 16, 15], 1160, 576), ([250, 0, 0, 0], 136, 192),
+       ([1] * 70, 72, 64)]
+MANY = [([700, 0, 513, 256, 1000], 264, 512), ([600], 100, 320), ([129, 1000, 511, 2000], 520, 1152),
+        ([900, 31, 0, 1500], 1160, 64)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts,n,k", FEW + MANY)
+def test_product(mxq, orc, fmt, counts, n, k):
+    ex = Experts(mxq, orc, fmt, counts, n, k, extra=5)
+    ex.check(mxq, torch.float32)
+    ex.check(mxq, torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts", [[3, 0, 140], [700, 5, 600]])
+def test_product_odd_columns_and_8bit_short_k(mxq, orc, fmt, counts):
+    """Rows of y that start at no 16-byte boundary, and one k-step of 32 bytes."""
+    Experts(mxq, orc, fmt, counts, 131, 64).check(mxq, torch.float32)
+    if fmt in (MXFP8, INT8_ROW, FP8_TENSOR):
+        Experts(mxq, orc, fmt, counts, 77, 96).check(mxq, torch.bfloat16)
+        Experts(mxq, orc, fmt, counts, 8, 32).check(mxq, torch.float32)
+
+
+def test_product_int8_is_qlinear_bit_for_bit(mxq, orc):
+    """Integer sums are exact, so each row has the bits mxq_qlinear gives it, split K or not, few rows or many."""
+    for counts, n, k in (([5, 0, 2], 256, 4608), ([1], 128, 4608), ([500, 700], 384, 1152)):
+        ex = Experts(mxq, orc, INT8_ROW, counts, n, k)
+        y = ex.run(mxq, torch.float32)
+        codes, scales = ex.xq.codes.view(-1, k), ex.xq.scales.view(-1, 4)
+        wc, ws = ex.w.codes.view(len(counts), n, k), ex.w.scales.view(len(counts), n * 4)
+        for e, c in enumerate(counts):
+            if not c:
+                continue
+            lo, hi = int(ex.off[e]), int(ex.off[e + 1])
+            a = mxq.QTensor(INT8_ROW, mxq.MMA, c, k, codes[lo:hi].clone(), scales[lo:hi].clone(), None)
+            b = mxq.QTensor(INT8_ROW, mxq.MMA, n, k, wc[e].clone(), ws[e].clone(), None)
+            assert torch.equal(mxq.qlinear(a, b, out_dtype=torch.float32), y[lo:hi])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts", [[1, 0, 7, 2], [700, 200, 0, 300]])
+def test_product_same_bits_twice_and_by_parts(mxq, orc, fmt, counts):
+    ex = Experts(mxq, orc, fmt, counts, 256, 2048)
+    y = ex.run(mxq, torch.float32)
+    assert torch.equal(y, ex.run(mxq, torch.float32))
+    # a part of the experts: offsets from the middle, that part's weight, scales laid out from its first group
+    first, n, k = 1, 256, 2048
+    off = ex.offsets[first:first + 2].clone()
+    lo, hi = int(off[0]), int(off[-1])
+    part = mxq.ExpertWeight(fmt, 1, n, k, ex.w.codes.view(4, -1)[1].clone(),
+                            None if ex.w.scales is None else ex.w.scales.view(4, -1)[1].clone(),
+                            None if ex.w.tensor_scales is None else ex.w.tensor_scales[1:2].clone())
+    q = mxq.QTensor(fmt, mxq.MMA, ex.xq.rows, k, ex.xq.codes, ex.xq.scales, ex.xq.tensor_scale)
+    if fmt in BLOCK:
+        sp, tile = (k // BLOCK[fmt] + 15) // 16 * 16, (counts[0] + 127) // 128
+        q.scales = torch.zeros(mxq.grouped_scales_bytes(fmt, ex.xq.rows, 1, k), dtype=torch.uint8, device="cuda")
+        src = ex.xq.scales[128 * sp * tile:128 * sp * (tile + (hi - lo + 127) // 128)]
+        q.scales[:src.numel()] = src
+    z = torch.full_like(y, 3.0)
+    mxq.qlinear_grouped(q, part, off, out=z)
+    assert mxq.check() == 0
+    gemm_close(z[lo:hi].cpu().numpy(), ex.ref[lo:hi]) if hi > lo else None
+    assert (z[:lo] == 3.0).all() and (z[hi:] == 3.0).all()
+
+
+@pytest.mark.parametrize("bad", [[0, 5, 3, 20], [-7, 2, 2, 20], [0, 4, 90, 20], [19, 4, 4, 4], [2 ** 31 - 1] * 4])
+@pytest.mark.parametrize("fmt", [MXFP8, INT8_ROW])
+@pytest.mark.parametrize("scale", [1, 40])
+def test_offsets_out_of_order_are_clamped_and_reported(mxq, orc, bad, fmt, scale):
+    """No access leaves the buffers (the kernels clamp each offset) and the next check says so, once."""
+    ex = Experts(mxq, orc, fmt, [8 * scale, 8 * scale, 4 * scale], 128, 256)
+    off = torch.tensor([min(v * scale, 2 ** 31 - 1) for v in bad], dtype=torch.int32, device="cuda")
+    mxq.qlinear_grouped(ex.xq, ex.w, off)
+    assert mxq.check() == 1 and mxq.check() == 0
+    q = mxq.alloc_grouped(fmt, 20 * scale, 3, 256)
+    x = torch.randn(20 * scale, 256, device="cuda")
+    mxq.quantize_grouped(x, fmt, off, out=q)
+    assert mxq.check() == (0 if fmt == INT8_ROW else 1) and mxq.check() == 0
+    ex.check(mxq, torch.float32)
+
+
+# ------------------------------------------------------------------ combine
+
+@pytest.mark.parametrize("ydt,odt", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("tokens,topk,n", [(1, 1, 1), (3, 8, 264), (200, 4, 100), (17, 5, 131), (64, 32, 8), (1000, 2, 1152)])
+def test_combine(mxq, ydt, odt, tokens, topk, n):
+    rng = np.random.default_rng(tokens + n)
+    e = max(topk, 8)
+    off, slot = ref_plan(routing(rng, tokens, topk, e, 0.3 if tokens > 1 else 0.0), e)
+    y = host_values(rng.standard_normal((tokens * topk, n)).astype(np.float32), ydt)
+    w = rng.random((tokens, topk)).astype(np.float32)
+    yd = dev(y, ydt)
+    yd[int(off[-1]):] = float("nan")                      # rows behind the last group
+    for weights in (w, None):
+        out = mxq.expert_combine(yd, torch.from_numpy(slot).cuda(), None if weights is None else torch.from_numpy(w).cuda(),
+                                 out_dtype=torch.bfloat16 if odt == "bf16" else torch.float32)
+        assert mxq.check() == 0
+        terms = np.where(slot >= 0, w if weights is not None else 1.0, 0.0)[..., None] * y.astype(np.float64)[np.maximum(slot, 0)]
+        ref, mag = terms.sum(1), np.abs(terms).sum(1)
+        got = out.float().cpu().numpy().astype(np.float64)
+        tol = topk * 2.0 ** -24 * mag * (1 + 1e-6) + (2.0 ** -8 * (np.abs(ref) + 1e-6 * mag) if odt == "bf16" else 0)
+        assert (np.abs(got - ref) <= tol).all()
+        assert (got[(slot < 0).all(1)] == 0).all()
+
+
+def test_combine_slots_outside_are_left_out_and_reported(mxq):
+    y = torch.ones(4, 16, device="cuda")
+    slot = torch.tensor([[0, 4], [2 ** 31 - 1, -2 ** 31], [3, 1]], dtype=torch.int32, device="cuda")
+    out = mxq.expert_combine(y, slot)
+    assert mxq.check() == 1 and mxq.check() == 0
+    assert out[:, 0].tolist() == [1.0, 0.0, 2.0]
+    assert (mxq.expert_combine(y[:0], torch.full((2, 3), -1, dtype=torch.int32, device="cuda")) == 0).all()
+
+
+# ------------------------------------------------------------------ together
+
+def layer(mxq, x, ids, weights, w, fmt, n):
+    """One linear of a mixture of experts, as a user runs it."""
+    plan = mxq.expert_plan(ids, n)
+    xq = mxq.quantize_grouped(x, fmt, plan.offsets, plan.slot)
+    return mxq.expert_combine(mxq.qlinear_grouped(xq, w, plan.offsets), plan.slot, weights)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("tokens,topk,e", [(1, 2, 8), (40, 4, 16), (900, 3, 6)])
+def test_layer(mxq, orc, fmt, tokens, topk, e):
+    rng = np.random.default_rng(tokens + fmt)
+    n, k = 264, 320
+    x = workloads.to_bf16_values(rng.standard_normal((tokens, k)).astype(np.float32))
+    w = workloads.to_bf16_values((rng.standard_normal((e, n, k)) * 0.05).astype(np.float32))
+    ids = routing(rng, tokens, topk, e, 0.0)
+    gate = rng.random((tokens, topk)).astype(np.float32)
+    we = mxq.prepare_experts(dev(w, "bf16"), fmt)
+    args = (dev(x, "bf16"), torch.from_numpy(ids).cuda(), torch.from_numpy(gate).cuda(), we, fmt, e)
+    y = layer(mxq, *args)
+    assert mxq.check() == 0
+    xv = deq64(orc.quantize(x, fmt))
+    ref, mag = np.zeros((tokens, n)), np.zeros((tokens, n))
+    for i in range(e):
+        t, j = np.nonzero(ids == i)
+        part = gate[t, j, None] * (xv[t] @ deq64(orc.quantize(w[i], fmt)).T)
+        np.add.at(ref, t, part)
+        np.add.at(mag, t, np.abs(part))
+    got = y.float().cpu().numpy()
+    # each product rounded to bf16 once (2^-8 of it), the sum once more; fp32 sums as in gemm_close
+    assert (np.abs(got - ref) <= 2.0 ** -8 * (mag + np.abs(ref)) + 1e-4 * np.abs(ref).max()).all()
+    # captured once, replayed on other inputs; and the same on a stream of its own
+    static = [a.clone() for a in args[:3]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        z = layer(mxq, *static, *args[3:])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side, capture_error_mode="thread_local"):
+            out = layer(mxq, *static, *args[3:])
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(z, y)
+    static[1].copy_(static[1].flip(0))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, layer(mxq, static[0], static[1], static[2], *args[3:]))
+    assert mxq.check() == 0
+
+
+def test_two_captured_layers_in_flight(mxq):
+    """Two captured layers replayed on two streams share nothing."""
+    n, k, e = 128, 128, 8
+    runs = []
+    for seed in (1, 2):
+        torch.manual_seed(seed)
+        x = torch.randn(64, k, device="cuda", dtype=torch.bfloat16)
+        ids = torch.randint(0, e, (64, 2), device="cuda")
+        w = mxq.prepare_experts(torch.randn(e, n, k, device="cuda") * 0.05, NVFP4)
+        gate = torch.rand(64, 2, device="cuda")
+        want = layer(mxq, x, ids, gate, w, NVFP4, e)
+        g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s, capture_error_mode="thread_local"):
+            out = layer(mxq, x, ids, gate, w, NVFP4, e)
+        runs.append((g, s, out, want, (x, ids, w, gate)))
+    for _ in range(20):
+        for g, s, _, _, _ in runs:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, _, out, want, _ in runs:
+        assert torch.equal(out, want)
+    assert mxq.check() == 0
+
+
+def test_stream_argument(mxq):
+    s = torch.cuda.Stream()
+    ids = torch.randint(0, 4, (50, 2), device="cuda")
+    torch.cuda.synchronize()
+    a, b = mxq.expert_plan(ids, 4, stream=s), mxq.expert_plan(ids, 4)
+    torch.cuda.synchronize()
+    assert torch.equal(a.offsets, b.offsets) and torch.equal(a.slot, b.slot)
