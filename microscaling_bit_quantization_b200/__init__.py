@@ -667,52 +667,62 @@ def _placed(f):
     """Runs f with its first tensor's device, and `stream`, as the current ones."""
     @functools.wraps(f)
     def call(x, *args, stream=None, **kwargs):
-        dev = x.codes.device if isinstance(x, QTensor) else x.device
-        if dev.type != "cuda":
+        t = x.codes if type(x) is QTensor else x
+        index = t.get_device()
+        if index < 0:
             raise ValueError("tensors must be on a CUDA device (there is no CPU path)")
         if stream is not None:
-            if stream.device != dev:
-                raise ValueError("stream of %s for tensors of %s" % (stream.device, dev))
+            if stream.device != t.device:
+                raise ValueError("stream of %s for tensors of %s" % (stream.device, t.device))
             with torch.cuda.stream(stream):
                 return f(x, *args, **kwargs)
-        if dev.index != torch.cuda.current_device():
-            with torch.cuda.device(dev):
+        if index != torch.cuda.current_device():
+            with torch.cuda.device(index):
                 return f(x, *args, **kwargs)
         return f(x, *args, **kwargs)
     return call
 
 
-def _want(t: Optional[torch.Tensor], what: str, dtype, dev, shape=None, numel=None):
-    """The address of a contiguous device tensor, or None; raises on anything else."""
+def _want(t: Optional[torch.Tensor], what: str, dtype, index: int, shape=None):
+    """The address of a contiguous tensor of device `index`, or None; raises on anything else."""
     if t is None:
         return None
-    if t.dtype != dtype:
-        raise TypeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
-    if t.device != dev:
-        raise ValueError("%s is on %s, not %s" % (what, t.device, dev))
-    if not t.is_contiguous():
-        raise ValueError("%s has to be contiguous" % what)
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError("%s has shape %s, not %s" % (what, tuple(t.shape), shape))
-    if numel is not None and t.numel() < numel:
-        raise ValueError("%s has %d elements, fewer than %d" % (what, t.numel(), numel))
-    return t.data_ptr() if t.numel() else None
+    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        if t.dtype is not dtype:
+            raise TypeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+        raise ValueError("%s: a contiguous tensor%s on device %d is wanted, got %s with strides %s on %s" %
+                         (what, "" if shape is None else " of shape %s" % (shape,), index, tuple(t.shape), t.stride(), t.device))
+    return t.data_ptr()
+
+
+def _bytes(t: Optional[torch.Tensor], what: str, need: int, index: int):
+    """The address of a contiguous tensor of at least `need` bytes, or None where none are needed."""
+    if need == 0:
+        return None
+    if t is None or t.get_device() != index or not t.is_contiguous() or t.numel() * t.element_size() < need:
+        raise ValueError("%s: %d contiguous bytes on device %d are wanted" % (what, need, index))
+    return t.data_ptr()
 
 
 def _raw_stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-def _plain_qtensor(q: QTensor, fmt: int, layout: int, rows: int, cols: int, scales_bytes_: int, dev, what: str):
-    """Checks a QTensor's sizes; returns its three addresses."""
-    if (q.fmt, q.layout, q.rows, q.cols) != (fmt, layout, rows, cols):
-        raise ValueError("%s: a %s tensor of %d x %d in layout %d is wanted" % (what, FORMAT_NAMES[fmt], rows, cols, layout))
-    for name, t, need in (("codes", q.codes, rows * cols // (2 if fmt in (MXFP4, NVFP4) else 1)),
-                          ("scales", q.scales, scales_bytes_), ("tensor_scale", q.tensor_scale,
-                                                                4 if fmt in (NVFP4, FP8_TENSOR) else 0)):
-        if need and (t is None or t.device != dev or not t.is_contiguous() or t.numel() * t.element_size() < need):
-            raise ValueError("%s.%s: %d contiguous bytes on %s are wanted" % (what, name, need, dev))
-    return _ptr(q.codes), _ptr(q.scales), _ptr(q.tensor_scale)
+@functools.lru_cache(maxsize=1024)
+def _sizes(fmt: int, layout: int, rows: int, n_groups: int, cols: int):
+    """Bytes of codes, scales (grouped when n_groups) and tensor scale."""
+    return (codes_bytes(fmt, rows, cols, layout),
+            grouped_scales_bytes(fmt, rows, n_groups, cols) if n_groups else scales_bytes(fmt, rows, cols, layout),
+            4 if fmt in (NVFP4, FP8_TENSOR) else 0)
+
+
+def _addresses(q: QTensor, fmt: int, layout: int, rows: int, n_groups: int, cols: int, index: int, what: str):
+    """Checks a QTensor against what a call needs; its three addresses."""
+    if q.fmt != fmt or q.layout != layout or q.rows != rows or q.cols != cols:
+        raise ValueError("%s: a %s tensor of %d x %d in layout %d is wanted" % (what, FORMAT_NAMES.get(fmt, fmt), rows, cols, layout))
+    c, s, t = _sizes(fmt, layout, rows, n_groups, cols)
+    return (_bytes(q.codes, what + ".codes", c, index), _bytes(q.scales, what + ".scales", s, index),
+            _bytes(q.tensor_scale, what + ".tensor_scale", t, index))
 
 
 @dataclass
@@ -731,22 +741,25 @@ def expert_plan_workspace_bytes(rows: int, n_experts: int) -> int:
 def expert_plan(expert_ids: torch.Tensor, n_experts: int, out: ExpertPlan = None,
                 workspace: torch.Tensor = None) -> ExpertPlan:
     """Plan of a routing: expert_ids int32/int64 [tokens, topk], ids outside [0, n_experts) dropped."""
-    if expert_ids.dtype not in (torch.int32, torch.int64) or expert_ids.dim() != 2:
+    ids, index = expert_ids.contiguous(), expert_ids.get_device()
+    wide = ids.dtype is torch.int64
+    if not wide and ids.dtype is not torch.int32 or ids.dim() != 2:
         raise TypeError("expert_ids: a 2-D int32 or int64 tensor is wanted")
-    ids, dev = expert_ids.contiguous(), expert_ids.device
-    rows = ids.numel()
+    rows, shape = ids.numel(), ids.shape
     if out is None:
-        out = ExpertPlan(torch.empty(n_experts + 1, dtype=torch.int32, device=dev),
-                         torch.empty(ids.shape, dtype=torch.int32, device=dev))
-    need = expert_plan_workspace_bytes(rows, n_experts)
+        out = ExpertPlan(torch.empty(n_experts + 1, dtype=torch.int32, device=ids.device),
+                         torch.empty(shape, dtype=torch.int32, device=ids.device))
+    need = _plan_bytes(rows, n_experts)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _ok(_lib.mxq_expert_plan(_ptr(ids), 64 if ids.dtype == torch.int64 else 32, rows, n_experts,
-                             _want(out.offsets, "offsets", torch.int32, dev, (n_experts + 1,)),
-                             _want(out.slot, "slot", torch.int32, dev, tuple(ids.shape)),
-                             _want(workspace, "workspace", torch.uint8, dev) if need else None,
-                             workspace.numel() if need else 0, _raw_stream()), "mxq_expert_plan")
+        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
+    _ok(_lib.mxq_expert_plan(ids.data_ptr(), 64 if wide else 32, rows, n_experts,
+                             _want(out.offsets, "offsets", torch.int32, index, (n_experts + 1,)),
+                             _want(out.slot, "slot", torch.int32, index, shape),
+                             _bytes(workspace, "workspace", need, index), need, _raw_stream()), "mxq_expert_plan")
     return out
+
+
+_plan_bytes = functools.lru_cache(maxsize=1024)(expert_plan_workspace_bytes)
 
 
 def grouped_scales_bytes(fmt: int, rows: int, n_groups: int, cols: int) -> int:
@@ -766,7 +779,7 @@ def quantize_grouped(x: torch.Tensor, fmt: int, offsets: torch.Tensor, slot: tor
                      out: QTensor = None, workspace: torch.Tensor = None) -> QTensor:
     """Quantizes tokens x [tokens, cols] into expert order (slot int32
     [tokens, topk]), or rows that are in expert order already (slot None)."""
-    dev = x.device
+    index = x.get_device()
     if x.dim() != 2 or not x.is_contiguous():
         raise ValueError("x: a contiguous 2-D tensor is wanted")
     tokens, cols = x.shape
@@ -778,18 +791,17 @@ def quantize_grouped(x: torch.Tensor, fmt: int, offsets: torch.Tensor, slot: tor
         topk = slot.shape[1]
     rows = out.rows if out is not None else tokens * topk
     if out is None:
-        out = alloc_grouped(fmt, rows, n_groups, cols, dev)
-    codes, scales, ts = _plain_qtensor(out, fmt, MMA, rows, cols, grouped_scales_bytes(fmt, rows, n_groups, cols), dev, "out")
+        out = alloc_grouped(fmt, rows, n_groups, cols, x.device)
+    codes, scales, ts = _addresses(out, fmt, MMA, rows, n_groups, cols, index, "out")
     wsb = 0
-    if fmt in (NVFP4, FP8_TENSOR):
+    if ts is not None:
         wsb = quantize_workspace_bytes(fmt)
         if workspace is None:
-            workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
-    _ok(_lib.mxq_quantize_grouped(_ptr(x), _dtype_code(x), tokens, cols, fmt, hadamard_b,
-                                  _want(offsets, "offsets", torch.int32, dev), n_groups,
-                                  _want(slot, "slot", torch.int32, dev), topk, rows, codes, scales, ts,
-                                  _want(workspace, "workspace", torch.uint8, dev, numel=wsb) if wsb else None, wsb,
-                                  _raw_stream()), "mxq_quantize_grouped")
+            workspace = torch.empty(wsb, dtype=torch.uint8, device=x.device)
+    _ok(_lib.mxq_quantize_grouped(x.data_ptr(), _dtype_code(x), tokens, cols, fmt, hadamard_b,
+                                  _want(offsets, "offsets", torch.int32, index), n_groups,
+                                  _want(slot, "slot", torch.int32, index), topk, rows, codes, scales, ts,
+                                  _bytes(workspace, "workspace", wsb, index), wsb, _raw_stream()), "mxq_quantize_grouped")
     return out
 
 
@@ -809,6 +821,7 @@ class ExpertWeight:
                               _ptr(self.tensor_scales))
 
 
+@functools.lru_cache(maxsize=1024)
 def expert_weight_bytes(fmt: int, n_experts: int, rows: int, cols: int):
     out = (ctypes.c_size_t * 2)()
     _ok(_lib.mxq_expert_weight_bytes(fmt, n_experts, rows, cols, out), "mxq_expert_weight_bytes")
@@ -838,13 +851,16 @@ def prepare_experts(w: torch.Tensor, fmt: int, hadamard_b: int = 0) -> ExpertWei
 def qlinear_grouped(xq: QTensor, w: ExpertWeight, offsets: torch.Tensor, out_dtype=torch.bfloat16,
                     out: torch.Tensor = None) -> torch.Tensor:
     """y[r] = deq(xq)[r] . deq(w[expert of row r])^T for the rows of every expert; other rows of `out` stay."""
-    dev = xq.codes.device
+    index, rows, n, e = xq.codes.get_device(), xq.rows, w.rows, w.n_experts
     if out is None:
-        out = torch.empty((xq.rows, w.rows), dtype=out_dtype, device=dev)
-    xc, wc = xq.c(), w.c()
-    _ok(_lib.mxq_qlinear_grouped(ctypes.byref(xc), _want(offsets, "offsets", torch.int32, dev, (w.n_experts + 1,)),
-                                 ctypes.byref(wc), _want(out, "out", out.dtype, dev, (xq.rows, w.rows)),
-                                 _dtype_code(out), _raw_stream()), "mxq_qlinear_grouped")
+        out = torch.empty((rows, n), dtype=out_dtype, device=xq.codes.device)
+    xc = _QTensorC(xq.fmt, xq.layout, rows, xq.cols, *_addresses(xq, xq.fmt, MMA, rows, e, xq.cols, index, "xq"))
+    cb, sb = expert_weight_bytes(w.fmt, e, n, w.cols)
+    wc = _ExpertWeightC(w.fmt, e, n, w.cols, _bytes(w.codes, "w.codes", cb, index), _bytes(w.scales, "w.scales", sb, index),
+                        _bytes(w.tensor_scales, "w.tensor_scales", 4 * e if w.fmt in (NVFP4, FP8_TENSOR) else 0, index))
+    _ok(_lib.mxq_qlinear_grouped(xc, _want(offsets, "offsets", torch.int32, index, (e + 1,)), wc,
+                                 _want(out, "out", out.dtype, index, (rows, n)), _dtype_code(out), _raw_stream()),
+        "mxq_qlinear_grouped")
     return out
 
 
@@ -852,17 +868,17 @@ def qlinear_grouped(xq: QTensor, w: ExpertWeight, offsets: torch.Tensor, out_dty
 def expert_combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = None, out_dtype=None,
                    out: torch.Tensor = None) -> torch.Tensor:
     """out[t] = sum_i weights[t, i] y[slot[t, i]] (weights None: 1; dropped choices left out)."""
-    dev = y.device
+    index = y.get_device()
     if y.dim() != 2 or slot.dim() != 2:
         raise ValueError("y and slot: 2-D tensors are wanted")
     rows, n = y.shape
     tokens, topk = slot.shape
     if out is None:
-        out = torch.empty((tokens, n), dtype=out_dtype or y.dtype, device=dev)
-    _ok(_lib.mxq_expert_combine(_want(y, "y", y.dtype, dev), _dtype_code(y), rows, n,
-                                _want(slot, "slot", torch.int32, dev),
-                                _want(weights, "weights", torch.float32, dev, (tokens, topk)), tokens, topk,
-                                _want(out, "out", out.dtype, dev, (tokens, n)), _dtype_code(out), _raw_stream()),
+        out = torch.empty((tokens, n), dtype=out_dtype or y.dtype, device=y.device)
+    _ok(_lib.mxq_expert_combine(_want(y, "y", y.dtype, index), _dtype_code(y), rows, n,
+                                _want(slot, "slot", torch.int32, index),
+                                _want(weights, "weights", torch.float32, index, (tokens, topk)), tokens, topk,
+                                _want(out, "out", out.dtype, index, (tokens, n)), _dtype_code(out), _raw_stream()),
         "mxq_expert_combine")
     return out
 
@@ -870,32 +886,34 @@ def expert_combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = 
 # ---------------------------------------------------------------------------
 # Query and key heads behind the q/k/v linear.
 
-def _token_stride(x: torch.Tensor, what: str) -> int:
+def _token_stride(x: torch.Tensor, what: str, shape, dtype, index: int) -> int:
     """Elements between the tokens of [tokens, heads, dim] whose heads lie one after the other."""
-    t, h, d = x.shape
-    if d > 1 and x.stride(2) != 1 or h > 1 and x.stride(1) != d:
-        raise ValueError("%s: the heads of a token have to lie one after the other" % what)
-    return x.stride(0) if t > 1 else h * d
+    t, h, d = shape
+    s = x.stride()
+    if x.shape != shape or x.dtype is not dtype or x.get_device() != index or len(s) != 3 or \
+            d > 1 and s[2] != 1 or h > 1 and s[1] != d:
+        raise ValueError("%s: %s %s on device %d with the heads of a token one after the other is wanted" %
+                         (what, dtype, tuple(shape), index))
+    return s[0] if t > 1 else h * d
 
 
 def _heads(q, k, q_weight, k_weight, cos, sin, positions, eps, norm, interleaved) -> _HeadsC:
-    dev = q.device
-    if q.dim() != 3 or (k is not None and (k.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2] or
-                                           k.dtype != q.dtype or k.device != dev)):
-        raise ValueError("q and k: [tokens, heads, head_dim] of one type and device are wanted")
+    index, dtype = q.get_device(), q.dtype
+    if q.dim() != 3 or k is not None and k.dim() != 3:
+        raise ValueError("q and k: [tokens, heads, head_dim] is wanted")
     tokens, hq, d = q.shape
+    hk = 0 if k is None else k.shape[1]
     n_pos, half = (0, 0) if cos is None else cos.shape
     if cos is not None and (sin is None or sin.shape != cos.shape):
         raise ValueError("sin: the shape of cos is wanted")
-    if positions is not None and positions.dtype not in (torch.int32, torch.int64):
-        raise TypeError("positions: int32 or int64 is wanted")
+    wide = positions is not None and positions.dtype is torch.int64
     f32 = torch.float32
-    return _HeadsC(_ptr(q), _ptr(k), _token_stride(q, "q"), 0 if k is None else _token_stride(k, "k"), hq,
-                   0 if k is None else k.shape[1], d, _dtype_code(q), tokens, NORMS[norm], eps,
-                   _want(q_weight, "q_weight", f32, dev, (d,)), _want(k_weight, "k_weight", f32, dev, (d,)), 2 * half,
-                   int(interleaved), _want(cos, "cos", f32, dev), _want(sin, "sin", f32, dev), n_pos,
-                   None if positions is None else _want(positions, "positions", positions.dtype, dev, (tokens,)),
-                   64 if positions is not None and positions.dtype == torch.int64 else 32)
+    return _HeadsC(q.data_ptr(), None if k is None else k.data_ptr(), _token_stride(q, "q", q.shape, dtype, index),
+                   0 if k is None else _token_stride(k, "k", (tokens, hk, d), dtype, index), hq, hk, d, _dtype_code(q), tokens,
+                   NORMS[norm], eps, _want(q_weight, "q_weight", f32, index, (d,)),
+                   _want(k_weight, "k_weight", f32, index, (d,)), 2 * half, interleaved, _want(cos, "cos", f32, index),
+                   _want(sin, "sin", f32, index), n_pos,
+                   _want(positions, "positions", torch.int64 if wide else torch.int32, index, (tokens,)), 64 if wide else 32)
 
 
 @_placed
@@ -911,12 +929,11 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor = None, q_weight: torch.Tensor
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k_out is None and k is not None:
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    for x, o, what in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-        if x is not None and (o.shape != x.shape or o.dtype != x.dtype or o.device != x.device):
-            raise ValueError("%s: %s %s on %s is wanted" % (what, x.dtype, tuple(x.shape), x.device))
-    _ok(_lib.mxq_qk_norm_rope(ctypes.byref(h), _ptr(q_out), _token_stride(q_out, "q_out"),
-                              _ptr(k_out) if k is not None else None,
-                              _token_stride(k_out, "k_out") if k is not None else 0, _raw_stream()), "mxq_qk_norm_rope")
+    index = q.get_device()
+    _ok(_lib.mxq_qk_norm_rope(h, q_out.data_ptr(), _token_stride(q_out, "q_out", q.shape, q.dtype, index),
+                              None if k is None else k_out.data_ptr(),
+                              0 if k is None else _token_stride(k_out, "k_out", k.shape, k.dtype, index), _raw_stream()),
+        "mxq_qk_norm_rope")
     return q_out, k_out
 
 
@@ -930,20 +947,17 @@ def qk_norm_rope_quantize(q: torch.Tensor, k: torch.Tensor = None, q_weight: tor
     codes in fmt (MXFP8, MXFP4, INT8_ROW; canonical layout, row
     token * heads + head).  Returns (QTensor of q, QTensor of k)."""
     h = _heads(q, k, q_weight, k_weight, cos, sin, positions, eps, norm, interleaved)
-    ptrs, res = [], []
-    for x, o, what in ((q, q_out, "q_out"), (k, k_out, "k_out")):
-        if x is None:
-            ptrs += [None, None]
-            res.append(None)
-            continue
-        rows, d = x.shape[0] * x.shape[1], x.shape[2]
-        if o is None:
-            o = alloc_qtensor(fmt, rows, d, CANONICAL, x.device)
-        ptrs += _plain_qtensor(o, fmt, CANONICAL, rows, d, scales_bytes(fmt, rows, d), x.device, what)[:2]
-        res.append(o)
-    _ok(_lib.mxq_qk_norm_rope_quantize(ctypes.byref(h), fmt, hadamard_b, *ptrs, _raw_stream()),
-        "mxq_qk_norm_rope_quantize")
-    return tuple(res)
+    index, d = q.get_device(), q.shape[2]
+    if q_out is None:
+        q_out = alloc_qtensor(fmt, q.shape[0] * q.shape[1], d, CANONICAL, q.device)
+    qc, qs, _ = _addresses(q_out, fmt, CANONICAL, q.shape[0] * q.shape[1], 0, d, index, "q_out")
+    kc = ks = None
+    if k is not None:
+        if k_out is None:
+            k_out = alloc_qtensor(fmt, k.shape[0] * k.shape[1], d, CANONICAL, k.device)
+        kc, ks, _ = _addresses(k_out, fmt, CANONICAL, k.shape[0] * k.shape[1], 0, d, index, "k_out")
+    _ok(_lib.mxq_qk_norm_rope_quantize(h, fmt, hadamard_b, qc, qs, kc, ks, _raw_stream()), "mxq_qk_norm_rope_quantize")
+    return q_out, (k_out if k is not None else None)
 
 
 def check(stream=None) -> int:

@@ -39,130 +39,228 @@ struct HeadKernelArgs {
     unsigned int *err;
 };
 
-// Sum over the `units` lanes of a head; `u` is this lane's place among them
-// (lanes past the last head have u >= units and take no part).
+// Sum over the lanes of a head: UNITS neighbouring lanes, a power of two, or
+// (UNITS = 0) any number, `u` being this lane's place among them (lanes past
+// the last head have u >= units and take no part).
+template <int UNITS>
 __device__ __forceinline__ float head_sum(float x, int u, int units, int lane) {
-    for (int o = units > 16 ? 16 : units > 8 ? 8 : units > 4 ? 4 : units > 2 ? 2 : 1; o > 0; o >>= 1) {
-        const float y = __shfl_down_sync(0xFFFFFFFFu, x, o);
-        if (u < o && u + o < units) x += y;
-    }
-    return __shfl_sync(0xFFFFFFFFu, x, lane - u);
-}
-
-struct Raw4 {   // four elements as loaded
-    uint4 w;
-};
-__device__ __forceinline__ void load4(Raw4 &r, const __nv_bfloat16 *p) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    r.w.x = v.x;
-    r.w.y = v.y;
-}
-__device__ __forceinline__ void load4(Raw4 &r, const float *p) { r.w = *reinterpret_cast<const uint4 *>(p); }
-template <typename T>
-__device__ __forceinline__ void unpack4(const Raw4 &r, float *v) {
-    if (sizeof(T) == 2) {
-        v[0] = __uint_as_float(r.w.x << 16);
-        v[1] = __uint_as_float(r.w.x & 0xFFFF0000u);
-        v[2] = __uint_as_float(r.w.y << 16);
-        v[3] = __uint_as_float(r.w.y & 0xFFFF0000u);
-    } else {
-        v[0] = __uint_as_float(r.w.x);
-        v[1] = __uint_as_float(r.w.y);
-        v[2] = __uint_as_float(r.w.z);
-        v[3] = __uint_as_float(r.w.w);
-    }
-}
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float *v) {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-}
-__device__ __forceinline__ void store4(float *p, const float *v) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-
-// Where a lane's two groups of four elements lie in its head, and its angles.
-struct LanePlace {
-    int p0, p1;
-    bool turned;
-    float c[4], s[4];
-};
-__device__ __forceinline__ LanePlace place_of(const HeadArgs &h, int u, int64_t pos) {
-    LanePlace q;
-    q.turned = 8 * u < h.rot;
-    const bool split = q.turned && !h.interleaved;
-    q.p0 = split ? 4 * u : 8 * u;
-    q.p1 = split ? h.rot / 2 + 4 * u : 8 * u + 4;
+    if constexpr (UNITS > 0) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        q.c[i] = 1.0f;
-        q.s[i] = 0.0f;
+        for (int o = 1; o < UNITS; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+        return x;
+    } else {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float y = __shfl_down_sync(0xFFFFFFFFu, x, o);
+            if (u < o && u + o < units) x += y;
+        }
+        return __shfl_sync(0xFFFFFFFFu, x, lane - u);
     }
-    if (q.turned) {
+}
+
+// A lane's eight elements as the firsts a[0..3] and the seconds b[0..3] of
+// four pairs, two-wide for packed arithmetic.
+struct Pairs {
+    float2 a[2], b[2];
+};
+template <typename T>
+struct Raw {
+    uint4 w[sizeof(T) / 2];
+};
+template <bool IL>
+__device__ __forceinline__ void load_raw(Raw<__nv_bfloat16> &r, const __nv_bfloat16 *x, int p0, int p1) {
+    if (IL) {
+        r.w[0] = *reinterpret_cast<const uint4 *>(x + p0);
+    } else {
+        const uint2 a = *reinterpret_cast<const uint2 *>(x + p0), b = *reinterpret_cast<const uint2 *>(x + p1);
+        r.w[0] = make_uint4(a.x, a.y, b.x, b.y);
+    }
+}
+template <bool IL>
+__device__ __forceinline__ void load_raw(Raw<float> &r, const float *x, int p0, int p1) {
+    r.w[0] = *reinterpret_cast<const uint4 *>(x + p0);
+    r.w[1] = *reinterpret_cast<const uint4 *>(x + p1);
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+template <bool IL>
+__device__ __forceinline__ Pairs unpack(const Raw<__nv_bfloat16> &r) {
+    const uint4 w = r.w[0];
+    Pairs v;
+    if (IL) {
+        v.a[0] = make_float2(bf_lo(w.x), bf_lo(w.y));
+        v.a[1] = make_float2(bf_lo(w.z), bf_lo(w.w));
+        v.b[0] = make_float2(bf_hi(w.x), bf_hi(w.y));
+        v.b[1] = make_float2(bf_hi(w.z), bf_hi(w.w));
+    } else {
+        v.a[0] = make_float2(bf_lo(w.x), bf_hi(w.x));
+        v.a[1] = make_float2(bf_lo(w.y), bf_hi(w.y));
+        v.b[0] = make_float2(bf_lo(w.z), bf_hi(w.z));
+        v.b[1] = make_float2(bf_lo(w.w), bf_hi(w.w));
+    }
+    return v;
+}
+template <bool IL>
+__device__ __forceinline__ Pairs unpack(const Raw<float> &r) {
+    const uint4 x = r.w[0], y = r.w[1];
+    auto f = [](uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); };
+    Pairs v;
+    if (IL) {
+        v.a[0] = f(x.x, x.z);
+        v.b[0] = f(x.y, x.w);
+        v.a[1] = f(y.x, y.z);
+        v.b[1] = f(y.y, y.w);
+    } else {
+        v.a[0] = f(x.x, x.y);
+        v.a[1] = f(x.z, x.w);
+        v.b[0] = f(y.x, y.y);
+        v.b[1] = f(y.z, y.w);
+    }
+    return v;
+}
+// The elements at p0 .. p0 + 3 and p1 .. p1 + 3.
+template <bool IL>
+__device__ __forceinline__ void in_order(const Pairs &v, float4 &x, float4 &y) {
+    if (IL) {
+        x = make_float4(v.a[0].x, v.b[0].x, v.a[0].y, v.b[0].y);
+        y = make_float4(v.a[1].x, v.b[1].x, v.a[1].y, v.b[1].y);
+    } else {
+        x = make_float4(v.a[0].x, v.a[0].y, v.a[1].x, v.a[1].y);
+        y = make_float4(v.b[0].x, v.b[0].y, v.b[1].x, v.b[1].y);
+    }
+}
+template <bool IL>
+__device__ __forceinline__ void store_raw(__nv_bfloat16 *o, int p0, int p1, const Pairs &v) {
+    float4 x, y;
+    in_order<IL>(v, x, y);
+    const uint2 a = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    const uint2 b = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    if (IL) {
+        *reinterpret_cast<uint4 *>(o + p0) = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+        *reinterpret_cast<uint2 *>(o + p0) = a;
+        *reinterpret_cast<uint2 *>(o + p1) = b;
+    }
+}
+template <bool IL>
+__device__ __forceinline__ void store_raw(float *o, int p0, int p1, const Pairs &v) {
+    float4 x, y;
+    in_order<IL>(v, x, y);
+    *reinterpret_cast<float4 *>(o + p0) = x;
+    *reinterpret_cast<float4 *>(o + p1) = y;
+}
+
+// Weight and rotation of a lane's pairs as one linear map:
+// a' = aa a + ab b, b' = bb b + ba a with aa = w_a c, ab = -w_b s, bb = w_b c,
+// ba = w_a s; for elements behind rot_dim a' = w_a a, b' = w_b b.  It changes
+// with the token and from q to k only.
+struct Turn {
+    float2 aa[2], ab[2], bb[2], ba[2];
+};
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+template <bool IL>
+__device__ __forceinline__ Turn turn_of(const HeadArgs &h, const float *w, int u, int p0, int p1, bool turned, int64_t pos) {
+    float4 x = make_float4(1.0f, 1.0f, 1.0f, 1.0f), y = x;
+    if (w) {
+        x = __ldg(reinterpret_cast<const float4 *>(w + p0));
+        y = __ldg(reinterpret_cast<const float4 *>(w + p1));
+    }
+    Turn t;
+    if (IL) {
+        t.aa[0] = make_float2(x.x, x.z);
+        t.bb[0] = make_float2(x.y, x.w);
+        t.aa[1] = make_float2(y.x, y.z);
+        t.bb[1] = make_float2(y.y, y.w);
+    } else {
+        t.aa[0] = make_float2(x.x, x.y);
+        t.aa[1] = make_float2(x.z, x.w);
+        t.bb[0] = make_float2(y.x, y.y);
+        t.bb[1] = make_float2(y.z, y.w);
+    }
+    if (turned) {
         const int64_t at = pos * (h.rot / 2) + 4 * u;
         const float4 c = __ldg(reinterpret_cast<const float4 *>(h.cos_t + at));
         const float4 s = __ldg(reinterpret_cast<const float4 *>(h.sin_t + at));
-        q.c[0] = c.x; q.c[1] = c.y; q.c[2] = c.z; q.c[3] = c.w;
-        q.s[0] = s.x; q.s[1] = s.y; q.s[2] = s.z; q.s[3] = s.w;
-    }
-    return q;
-}
-
-__device__ __forceinline__ void turn(float &a, float &b, float c, float s) {
-    const float x = a, y = b;
-    a = fmaf(x, c, -(y * s));
-    b = fmaf(y, c, x * s);
-}
-
-// Norm and rotation of a lane's 8 elements v (group 0 then group 1).
-__device__ __forceinline__ void norm_rotate(float (&v)[8], const HeadArgs &h, const LanePlace &q, const float *w, int u,
-                                            int units, int lane, bool on) {
-    const float inv_d = 1.0f / (float)h.head_dim;
-    if (h.norm == 1) {
-        float sum = 0.0f;
+        const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+        const float2 ss[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
+        const float2 minus = make_float2(-1.0f, -1.0f);
 #pragma unroll
-        for (int i = 0; i < 8; i++) sum += v[i];
-        const float mean = head_sum(sum, u, units, lane) * inv_d;
-#pragma unroll
-        for (int i = 0; i < 8; i++) v[i] -= mean;
-    }
-    float sq = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) sq = fmaf(v[i], v[i], sq);
-    const float r = rsqrtf(fmaf(head_sum(sq, u, units, lane), inv_d, h.eps));
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] *= r;
-    if (w && on) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(w + q.p0)), b = __ldg(reinterpret_cast<const float4 *>(w + q.p1));
-        v[0] *= a.x; v[1] *= a.y; v[2] *= a.z; v[3] *= a.w;
-        v[4] *= b.x; v[5] *= b.y; v[6] *= b.z; v[7] *= b.w;
-    }
-    if (q.turned) {
-        if (h.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 4; i++) turn(v[2 * i], v[2 * i + 1], q.c[i], q.s[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; i++) turn(v[i], v[i + 4], q.c[i], q.s[i]);
+        for (int i = 0; i < 2; i++) {
+            t.ab[i] = mul2(mul2(t.bb[i], minus), ss[i]);
+            t.ba[i] = mul2(t.aa[i], ss[i]);
+            t.aa[i] = mul2(t.aa[i], cc[i]);
+            t.bb[i] = mul2(t.bb[i], cc[i]);
         }
     }
+    return t;
+}
+
+// Norm of the heads in a pass: v becomes its weighted and turned elements
+// before the head's factor r = 1/sqrt(mean square + eps), which is returned
+// (the map is linear: one multiplication less, and none waits for the sum).
+template <int UNITS>
+__device__ __forceinline__ float norm_turn(Pairs &v, const HeadArgs &h, const Turn &t, bool turned, int u, int units, int lane) {
+    const float inv_d = 1.0f / (float)h.head_dim;
+    if (h.norm == 1) {
+        const float2 s2 = __fadd2_rn(__fadd2_rn(v.a[0], v.a[1]), __fadd2_rn(v.b[0], v.b[1]));
+        const float m = -head_sum<UNITS>(s2.x + s2.y, u, units, lane) * inv_d;
+        const float2 mm = make_float2(m, m);
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            v.a[i] = __fadd2_rn(v.a[i], mm);
+            v.b[i] = __fadd2_rn(v.b[i], mm);
+        }
+    }
+    const float2 q2 = fma2(v.b[1], v.b[1], fma2(v.b[0], v.b[0], fma2(v.a[1], v.a[1], mul2(v.a[0], v.a[0]))));
+    const float r = rsqrtf(fmaf(head_sum<UNITS>(q2.x + q2.y, u, units, lane), inv_d, h.eps));
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        float2 a = mul2(t.aa[i], v.a[i]), b = mul2(t.bb[i], v.b[i]);
+        if (turned) {
+            a = fma2(t.ab[i], v.b[i], a);
+            b = fma2(t.ba[i], v.a[i], b);
+        }
+        v.a[i] = a;
+        v.b[i] = b;
+    }
+    return r;
 }
 
 // The position of token t, or -1 (reported) for one outside the tables.
 __device__ __forceinline__ int64_t position_of(const HeadArgs &h, int64_t t, unsigned int *err) {
+    if (h.rot == 0) return 0;
     const int64_t pos = !h.positions ? t
                         : h.pos64    ? static_cast<const int64_t *>(h.positions)[t]
                                      : (int64_t)static_cast<const int32_t *>(h.positions)[t];
-    if (h.rot == 0 || (pos >= 0 && pos < h.n_pos)) return pos;
+    if (pos >= 0 && pos < h.n_pos) return pos;
     latch_index_error(err);
     return -1;
 }
 
-template <typename T>
+// What a lane does in every head: its place and its two groups of elements.
+template <int UNITS, bool IL>
+struct LanePlace {
+    int u, sub, p0, p1;
+    bool in_pass, turned;
+    __device__ __forceinline__ LanePlace(const HeadKernelArgs &a, int lane) {
+        const int units = UNITS ? UNITS : a.units;
+        u = lane % units;
+        sub = lane / units;
+        in_pass = UNITS ? true : sub < a.per_pass;
+        if (!in_pass) u = 32;   // takes no part in a sum
+        turned = in_pass && 8 * u < a.h.rot;
+        p0 = turned && !IL ? 4 * u : 8 * u;
+        p1 = turned && !IL ? a.h.rot / 2 + 4 * u : 8 * u + 4;
+    }
+};
+
+template <typename T, int UNITS, bool IL>
 __global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope(HeadKernelArgs a) {
     const HeadArgs &h = a.h;
     const int lane = threadIdx.x & 31;
-    const int u = lane % a.units, sub = lane / a.units;   // place in the head, head of the pass
-    const bool in_pass = sub < a.per_pass;
-    const int heads = h.q_heads + h.k_heads;
+    const LanePlace<UNITS, IL> q(a, lane);
+    const int heads = h.q_heads + h.k_heads, d = h.head_dim;
     pdl_wait();
     pdl_launch_dependents();
     const int64_t total = h.tokens * a.items;
@@ -171,68 +269,63 @@ __global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope(HeadKernelArgs a)
         const int64_t t = it / a.items;
         const int pass0 = (int)(it - t * a.items) * a.per_item;
         const int pass1 = pass0 + a.per_item < a.passes ? pass0 + a.per_item : a.passes;
-        auto source = [&](int head) {   // start of the head
-            return head < h.q_heads ? (const T *)h.q + t * h.q_stride + (int64_t)head * h.head_dim
-                                    : (const T *)h.k + t * h.k_stride + (int64_t)(head - h.q_heads) * h.head_dim;
-        };
+        // head i of the token at qx + i d, or kx + i d for the k heads
+        const T *qx = (const T *)h.q + t * h.q_stride, *kx = (const T *)h.k + t * h.k_stride - (int64_t)h.q_heads * d;
+        T *qy = (T *)h.q_out + t * h.q_out_stride, *ky = (T *)h.k_out + t * h.k_out_stride - (int64_t)h.q_heads * d;
+        const int end = pass1 * a.per_pass < heads ? pass1 * a.per_pass : heads;
+        int head = q.in_pass ? pass0 * a.per_pass + q.sub : end;
+        Raw<T> next = {};
+        if (head < end) load_raw<IL>(next, (head < h.q_heads ? qx : kx) + (int64_t)head * d, q.p0, q.p1);
         const int64_t pos = position_of(h, t, a.err);
-        LanePlace q = place_of(h, in_pass ? u : 0, pos < 0 ? 0 : pos);
-        Raw4 next[2] = {};
-        int head = pass0 * a.per_pass + sub;
-        bool on = in_pass && head < heads;
-        if (on) {
-            const T *x = source(head);
-            load4(next[0], x + q.p0);
-            load4(next[1], x + q.p1);
-        }
+        Turn turn = {};
+        int side = -1;   // whose weight `turn` holds
         for (int pass = pass0; pass < pass1; pass++) {
-            float v[8] = {};
-            if (on) {
-                unpack4<T>(next[0], v);
-                unpack4<T>(next[1], v + 4);
-            }
-            const int this_head = head;
-            const bool this_on = on;
+            Pairs v = unpack<IL>(next);
+            const int now = head;
             head += a.per_pass;
-            on = in_pass && head < heads && pass + 1 < pass1;
-            if (on) {
-                const T *x = source(head);
-                load4(next[0], x + q.p0);
-                load4(next[1], x + q.p1);
+            if (head < end) load_raw<IL>(next, (head < h.q_heads ? qx : kx) + (int64_t)head * d, q.p0, q.p1);
+            const int is_k = now >= h.q_heads;
+            if (is_k != side && now < end) {
+                side = is_k;
+                turn = turn_of<IL>(h, is_k ? h.k_weight : h.q_weight, q.u, q.p0, q.p1, q.turned, pos < 0 ? 0 : pos);
             }
-            const bool is_q = this_head < h.q_heads;
-            norm_rotate(v, h, q, is_q ? h.q_weight : h.k_weight, in_pass ? u : 32, a.units, lane, this_on);
-            if (pos < 0) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) v[i] = __int_as_float(0x7FC00000);
-            }
-            if (this_on) {
+            float r = norm_turn<UNITS>(v, h, turn, q.turned, q.u, a.units, lane);
+            if (pos < 0) r = __int_as_float(0x7FC00000);
+            if (now < end) {
                 // a lane stores the elements it loaded and no others: q_out = q and k_out = k are allowed
-                T *y = is_q ? (T *)h.q_out + t * h.q_out_stride + (int64_t)this_head * h.head_dim
-                            : (T *)h.k_out + t * h.k_out_stride + (int64_t)(this_head - h.q_heads) * h.head_dim;
-                store4(y + q.p0, v);
-                store4(y + q.p1, v + 4);
+                const float2 rr = make_float2(r, r);
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    v.a[i] = mul2(v.a[i], rr);
+                    v.b[i] = mul2(v.b[i], rr);
+                }
+                store_raw<IL>((is_k ? ky : qy) + (int64_t)now * d, q.p0, q.p1, v);
             }
         }
     }
 }
 
 // The same, then an optional Hadamard rotation and the codes of every head.
-// Two passes' heads go through shared memory (fp32, at most 2 KB per warp) to
-// the 16-element chunks of the quantizers, one chunk per lane, so that a
-// quantization or Hadamard block lies in aligned neighbouring lanes.
-template <typename T, int F>
-__global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope_quantize(HeadKernelArgs a) {
-    __shared__ __align__(16) float buf[kHeadWarps][512];
+// Two passes' heads go through shared memory (fp32, in rows of 16 elements
+// and 4 of padding, which spreads a warp's 16-byte accesses over the banks)
+// to the 16-element chunks of the quantizers, one chunk per lane, so that a
+// quantization or Hadamard block lies in aligned neighbouring lanes.  The
+// head's factor and 1/sqrt(b) are applied where the codes are formed.
+template <typename T, int F, int UNITS, bool IL>
+__global__ void __launch_bounds__(kHeadThreads, 5) k_qk_norm_rope_quantize(HeadKernelArgs a) {
+    __shared__ __align__(16) float buf[kHeadWarps][32 * 20];
+    __shared__ float factor[kHeadWarps][64];
     const HeadArgs &h = a.h;
     const int lane = threadIdx.x & 31;
-    float *b = buf[threadIdx.x >> 5];
-    const int u = lane % a.units, sub = lane / a.units;
-    const bool in_pass = sub < a.per_pass;
-    const int heads = h.q_heads + h.k_heads;
-    const int chunks = h.head_dim / 16;                     // lanes per head when coding
-    const int chead = lane / chunks, cc = lane % chunks;    // head among the two passes', chunk of it
+    float *b = buf[threadIdx.x >> 5], *fac = factor[threadIdx.x >> 5];
+    const LanePlace<UNITS, IL> q(a, lane);
+    const int heads = h.q_heads + h.k_heads, d = h.head_dim;
+    const int chunks = UNITS ? UNITS / 2 : d / 16;                                  // lanes per head when coding
+    const int chead = lane / chunks, cc = lane - chead * chunks;                    // head of the two passes', chunk of it
     const float norm = h.hadamard_b ? __frsqrt_rn((float)h.hadamard_b) : 1.0f;
+    auto padded = [](int e) { return (e >> 4) * 20 + (e & 15); };
+    float *b0 = b + padded(q.sub * d + q.p0), *b1 = b + padded(q.sub * d + q.p1);   // this lane's elements, first pass
+    const int second = padded(a.per_pass * d);                                      // (per_pass d is a multiple of 32)
     pdl_wait();
     pdl_launch_dependents();
     const int64_t total = h.tokens * a.items;
@@ -241,72 +334,80 @@ __global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope_quantize(HeadKern
         const int64_t t = it / a.items;
         const int pass0 = (int)(it - t * a.items) * a.per_item;
         const int pass1 = pass0 + a.per_item < a.passes ? pass0 + a.per_item : a.passes;
-        const int64_t pos = position_of(h, t, a.err);
-        const LanePlace q = place_of(h, in_pass ? u : 0, pos < 0 ? 0 : pos);
-        auto load = [&](int head, Raw4 (&r)[2]) {
-            if (!in_pass || head >= heads) return;
-            const T *x = head < h.q_heads ? (const T *)h.q + t * h.q_stride + (int64_t)head * h.head_dim
-                                          : (const T *)h.k + t * h.k_stride + (int64_t)(head - h.q_heads) * h.head_dim;
-            load4(r[0], x + q.p0);
-            load4(r[1], x + q.p1);
+        const T *qx = (const T *)h.q + t * h.q_stride, *kx = (const T *)h.k + t * h.k_stride - (int64_t)h.q_heads * d;
+        const int end = pass1 * a.per_pass < heads ? pass1 * a.per_pass : heads;
+        const int64_t qrow = t * h.q_heads, krow = t * h.k_heads - h.q_heads;   // row of head i: qrow + i or krow + i
+        int head = q.in_pass ? pass0 * a.per_pass + q.sub : end;
+        Raw<T> next[2] = {};
+        auto load = [&](int i, Raw<T> &r) {
+            if (i < end) load_raw<IL>(r, (i < h.q_heads ? qx : kx) + (int64_t)i * d, q.p0, q.p1);
         };
-        Raw4 next[2][2] = {};
-        int first = pass0 * a.per_pass;   // first head of the pair of passes
-        load(first + sub, next[0]);
-        if (pass0 + 1 < pass1) load(first + a.per_pass + sub, next[1]);
-        for (int pass = pass0; pass < pass1; pass += 2, first += 2 * a.per_pass) {
-            float v[2][8] = {};
+        load(head, next[0]);
+        load(head + a.per_pass, next[1]);
+        const int64_t pos = position_of(h, t, a.err);
+        Turn turn = {};
+        int side = -1;
+        for (int pass = pass0; pass < pass1; pass += 2) {
+            Pairs v[2] = {unpack<IL>(next[0]), unpack<IL>(next[1])};
+            load(head + 2 * a.per_pass, next[0]);
+            load(head + 3 * a.per_pass, next[1]);
+            __syncwarp();   // the chunks of the passes before have been read
 #pragma unroll
             for (int p = 0; p < 2; p++) {
-                unpack4<T>(next[p][0], v[p]);
-                unpack4<T>(next[p][1], v[p] + 4);
-            }
-            if (pass + 2 < pass1) load(first + 2 * a.per_pass + sub, next[0]);
-            if (pass + 3 < pass1) load(first + 3 * a.per_pass + sub, next[1]);
-            __syncwarp();
-#pragma unroll
-            for (int p = 0; p < 2; p++) {
-                const int head = first + p * a.per_pass + sub;
-                const bool on = in_pass && head < heads && pass + p < pass1;
-                norm_rotate(v[p], h, q, head < h.q_heads ? h.q_weight : h.k_weight, in_pass ? u : 32, a.units, lane, on);
-                if (on) {
-                    float *o = b + (p * a.per_pass + sub) * h.head_dim;
-                    *reinterpret_cast<float4 *>(o + q.p0) = make_float4(v[p][0], v[p][1], v[p][2], v[p][3]);
-                    *reinterpret_cast<float4 *>(o + q.p1) = make_float4(v[p][4], v[p][5], v[p][6], v[p][7]);
+                const int is_k = head >= h.q_heads;
+                if (is_k != side && head < end) {
+                    side = is_k;
+                    turn = turn_of<IL>(h, is_k ? h.k_weight : h.q_weight, q.u, q.p0, q.p1, q.turned, pos < 0 ? 0 : pos);
                 }
+                const float r = norm_turn<UNITS>(v[p], h, turn, q.turned, q.u, a.units, lane);
+                if (q.in_pass) {
+                    float4 x, y;
+                    in_order<IL>(v[p], x, y);
+                    *reinterpret_cast<float4 *>(b0 + p * second) = x;
+                    *reinterpret_cast<float4 *>(b1 + p * second) = y;
+                    if (q.u == 0) fac[p * a.per_pass + q.sub] = r * norm;
+                }
+                head += a.per_pass;
             }
             __syncwarp();
-            const int n_here = (pass + 1 < pass1 ? 2 : 1) * a.per_pass;
-            const int head = first + chead;
-            const bool valid = chead < n_here && head < heads;
+            const int chd = pass * a.per_pass + chead;
+            const bool valid = chead < 2 * a.per_pass && chd < end;
             float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; i++) x[i] = 0.0f;
-            if (valid) {
-                const float4 *src = reinterpret_cast<const float4 *>(b + lane * 16);
+            {
+                const float4 *src = reinterpret_cast<const float4 *>(b + lane * 20);
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const float4 f = src[i];
                     x[4 * i] = f.x; x[4 * i + 1] = f.y; x[4 * i + 2] = f.z; x[4 * i + 3] = f.w;
                 }
             }
-            if (h.hadamard_b) hadamard_chunk_n(x, h.hadamard_b, lane, norm);
-            float amax = amax16(x);
-            const bool is_q = head < h.q_heads;
-            const int64_t row = is_q ? t * h.q_heads + head : t * h.k_heads + (head - h.q_heads);
+            const float f = fac[chead & 63];
+            if (h.hadamard_b) hadamard_stages(x, h.hadamard_b, lane);
+            // the largest |x f| is |x|'s largest times f: rounding keeps the order
+            float amax = __fmul_rn(amax16(x), f);
+            const bool is_q = chd < h.q_heads;
+            const int64_t row = (is_q ? qrow : krow) + chd;
             uint8_t *codes = (uint8_t *)(is_q ? h.q_out : h.k_out);
             void *scales = is_q ? h.q_scales : h.k_scales;
             if (F == kINT8Row) {
-                for (int o = 16; o > 0; o >>= 1) {   // maximum over the head's lanes
-                    const float y = __shfl_down_sync(0xFFFFFFFFu, amax, o);
-                    if (cc < o && cc + o < chunks) amax = fmaxf(amax, y);
+                if (UNITS) {
+                    amax = group_max<(UNITS ? UNITS / 2 : 1)>(amax);
+                } else {
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) {   // maximum over the head's lanes
+                        const float y = __shfl_down_sync(0xFFFFFFFFu, amax, o);
+                        if (cc < o && cc + o < chunks) amax = fmaxf(amax, y);
+                    }
+                    amax = __shfl_sync(0xFFFFFFFFu, amax, (lane - cc) & 31);
                 }
-                amax = __shfl_sync(0xFFFFFFFFu, amax, (lane - cc) & 31);
                 const float s = pos < 0 ? __int_as_float(0x7FC00000) : __fdiv_rn(amax, 127.0f);
                 const Recip rs = recip_of(s);
                 if (valid) {
-                    uint4 w = make_uint4(int_x4_quot(x, rs, 127), int_x4_quot(x + 4, rs, 127), int_x4_quot(x + 8, rs, 127),
-                                         int_x4_quot(x + 12, rs, 127));
+                    float u[16];
+                    mul8(x, f, u);
+                    mul8(x + 8, f, u + 8);
+                    uint4 w = make_uint4(int_x4_quot(u, rs, 127), int_x4_quot(u + 4, rs, 127), int_x4_quot(u + 8, rs, 127),
+                                         int_x4_quot(u + 12, rs, 127));
                     if (pos < 0) w = make_uint4(0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u);   // 1 x NaN
                     *reinterpret_cast<uint4 *>(codes + (row * chunks + cc) * 16) = w;
                     if (cc == 0) reinterpret_cast<float *>(scales)[row] = s;
@@ -317,8 +418,17 @@ __global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope_quantize(HeadKern
                 float inv = 0.0f, z[16];
                 uint32_t sb = zero ? 127u : mx_scale(amax, F == kMXFP8 ? 8 : 2, inv);
                 if (pos < 0) sb = 255u;   // the NaN scale
-                mul8(x, inv, z);
-                mul8(x + 8, inv, z + 8);
+                // (x f) 2^-e rounded once, as x (f 2^-e) where that factor is finite and normal
+                const float m = __fmul_rn(f, inv);
+                if (m >= 1e-30f && m <= 1e30f) {
+                    mul8(x, m, z);
+                    mul8(x + 8, m, z + 8);
+                } else {
+                    mul8(x, f, z);
+                    mul8(x + 8, f, z + 8);
+                    mul8(z, inv, z);
+                    mul8(z + 8, inv, z + 8);
+                }
                 if (valid) {
                     if (F == kMXFP8) {
                         uint32_t w[4];
@@ -337,13 +447,11 @@ __global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope_quantize(HeadKern
                     if (!(cc & 1)) reinterpret_cast<uint8_t *>(scales)[row * (chunks / 2) + cc / 2] = (uint8_t)sb;
                 }
             }
-            __syncwarp();
         }
     }
 }
 
-template <typename F>
-cudaError_t launch_heads(F *k, const HeadKernelArgs &a, cudaStream_t s) {
+cudaError_t launch_heads(void (*k)(HeadKernelArgs), const HeadKernelArgs &a, cudaStream_t s) {
     const int64_t warps = a.h.tokens * a.items;
     int64_t ctas = (warps + kHeadWarps - 1) / kHeadWarps;
     const int64_t cap = (int64_t)sm_count() * 64;
@@ -356,6 +464,27 @@ cudaError_t launch_heads(F *k, const HeadKernelArgs &a, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k, a);
+}
+
+// The instance for a head's lanes (a power of two of them in registers'
+// butterflies, any other number by the shuffle tree) and its way of pairing.
+template <typename T, int UNITS, bool IL>
+cudaError_t pick_format(const HeadKernelArgs &a, cudaStream_t s) {
+    switch (a.h.fmt) {
+    case kMXFP8: return launch_heads(k_qk_norm_rope_quantize<T, kMXFP8, UNITS, IL>, a, s);
+    case kMXFP4: return launch_heads(k_qk_norm_rope_quantize<T, kMXFP4, UNITS, IL>, a, s);
+    case kINT8Row: return launch_heads(k_qk_norm_rope_quantize<T, kINT8Row, UNITS, IL>, a, s);
+    default: return launch_heads(k_qk_norm_rope<T, UNITS, IL>, a, s);
+    }
+}
+template <typename T, bool IL>
+cudaError_t pick_units(const HeadKernelArgs &a, cudaStream_t s) {
+    switch (a.units) {
+    case 8: return pick_format<T, 8, IL>(a, s);
+    case 16: return pick_format<T, 16, IL>(a, s);
+    case 32: return pick_format<T, 32, IL>(a, s);
+    default: return pick_format<T, 0, IL>(a, s);
+    }
 }
 
 }  // namespace
@@ -373,22 +502,14 @@ cudaError_t launch_qk_norm_rope(const HeadArgs &h, cudaStream_t s) {
     int64_t per = h.tokens * a.passes / want;
     per = per < 2 ? 2 : per > 16 ? 16 : per / 2 * 2;
     if (h.fmt < 0 && h.tokens * a.passes < want) per = 1;
-    a.per_item = (int)per;
+    a.items = (int)((a.passes + per - 1) / per);
+    per = (a.passes + a.items - 1) / a.items;   // a token's warps take equal shares
+    a.per_item = (int)(per == 1 ? 1 : (per + 1) / 2 * 2);
     a.items = (a.passes + a.per_item - 1) / a.per_item;
     const cudaError_t e = error_word_address(&a.err);
     if (e != cudaSuccess) return e;
-    if (h.fmt < 0) return h.bf16 ? launch_heads(k_qk_norm_rope<__nv_bfloat16>, a, s) : launch_heads(k_qk_norm_rope<float>, a, s);
-    switch (h.fmt) {
-    case kMXFP8:
-        return h.bf16 ? launch_heads(k_qk_norm_rope_quantize<__nv_bfloat16, kMXFP8>, a, s)
-                      : launch_heads(k_qk_norm_rope_quantize<float, kMXFP8>, a, s);
-    case kMXFP4:
-        return h.bf16 ? launch_heads(k_qk_norm_rope_quantize<__nv_bfloat16, kMXFP4>, a, s)
-                      : launch_heads(k_qk_norm_rope_quantize<float, kMXFP4>, a, s);
-    default:
-        return h.bf16 ? launch_heads(k_qk_norm_rope_quantize<__nv_bfloat16, kINT8Row>, a, s)
-                      : launch_heads(k_qk_norm_rope_quantize<float, kINT8Row>, a, s);
-    }
+    if (h.bf16) return h.interleaved ? pick_units<__nv_bfloat16, true>(a, s) : pick_units<__nv_bfloat16, false>(a, s);
+    return h.interleaved ? pick_units<float, true>(a, s) : pick_units<float, false>(a, s);
 }
 
 }  // namespace mxq
