@@ -704,8 +704,9 @@ def _bytes(t: Optional[torch.Tensor], what: str, need: int, index: int):
     return t.data_ptr()
 
 
-def _raw_stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+# The current stream's handle without a Stream object around it (3 us less per call), where torch has the call.
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -755,7 +756,7 @@ def expert_plan(expert_ids: torch.Tensor, n_experts: int, out: ExpertPlan = None
     _ok(_lib.mxq_expert_plan(ids.data_ptr(), 64 if wide else 32, rows, n_experts,
                              _want(out.offsets, "offsets", torch.int32, index, (n_experts + 1,)),
                              _want(out.slot, "slot", torch.int32, index, shape),
-                             _bytes(workspace, "workspace", need, index), need, _raw_stream()), "mxq_expert_plan")
+                             _bytes(workspace, "workspace", need, index), need, _stream_handle(index)), "mxq_expert_plan")
     return out
 
 
@@ -801,7 +802,7 @@ def quantize_grouped(x: torch.Tensor, fmt: int, offsets: torch.Tensor, slot: tor
     _ok(_lib.mxq_quantize_grouped(x.data_ptr(), _dtype_code(x), tokens, cols, fmt, hadamard_b,
                                   _want(offsets, "offsets", torch.int32, index), n_groups,
                                   _want(slot, "slot", torch.int32, index), topk, rows, codes, scales, ts,
-                                  _bytes(workspace, "workspace", wsb, index), wsb, _raw_stream()), "mxq_quantize_grouped")
+                                  _bytes(workspace, "workspace", wsb, index), wsb, _stream_handle(index)), "mxq_quantize_grouped")
     return out
 
 
@@ -843,7 +844,7 @@ def prepare_experts(w: torch.Tensor, fmt: int, hadamard_b: int = 0) -> ExpertWei
     ws = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
     wc = ew.c()
     _ok(_lib.mxq_expert_weight_prepare(_ptr(w), _dtype_code(w), hadamard_b, ctypes.byref(wc), _ptr(ws), wsb,
-                                       _raw_stream()), "mxq_expert_weight_prepare")
+                                       _stream_handle(w.get_device())), "mxq_expert_weight_prepare")
     return ew
 
 
@@ -859,7 +860,7 @@ def qlinear_grouped(xq: QTensor, w: ExpertWeight, offsets: torch.Tensor, out_dty
     wc = _ExpertWeightC(w.fmt, e, n, w.cols, _bytes(w.codes, "w.codes", cb, index), _bytes(w.scales, "w.scales", sb, index),
                         _bytes(w.tensor_scales, "w.tensor_scales", 4 * e if w.fmt in (NVFP4, FP8_TENSOR) else 0, index))
     _ok(_lib.mxq_qlinear_grouped(xc, _want(offsets, "offsets", torch.int32, index, (e + 1,)), wc,
-                                 _want(out, "out", out.dtype, index, (rows, n)), _dtype_code(out), _raw_stream()),
+                                 _want(out, "out", out.dtype, index, (rows, n)), _dtype_code(out), _stream_handle(index)),
         "mxq_qlinear_grouped")
     return out
 
@@ -878,7 +879,7 @@ def expert_combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = 
     _ok(_lib.mxq_expert_combine(_want(y, "y", y.dtype, index), _dtype_code(y), rows, n,
                                 _want(slot, "slot", torch.int32, index),
                                 _want(weights, "weights", torch.float32, index, (tokens, topk)), tokens, topk,
-                                _want(out, "out", out.dtype, index, (tokens, n)), _dtype_code(out), _raw_stream()),
+                                _want(out, "out", out.dtype, index, (tokens, n)), _dtype_code(out), _stream_handle(index)),
         "mxq_expert_combine")
     return out
 
@@ -932,7 +933,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor = None, q_weight: torch.Tensor
     index = q.get_device()
     _ok(_lib.mxq_qk_norm_rope(h, q_out.data_ptr(), _token_stride(q_out, "q_out", q.shape, q.dtype, index),
                               None if k is None else k_out.data_ptr(),
-                              0 if k is None else _token_stride(k_out, "k_out", k.shape, k.dtype, index), _raw_stream()),
+                              0 if k is None else _token_stride(k_out, "k_out", k.shape, k.dtype, index), _stream_handle(index)),
         "mxq_qk_norm_rope")
     return q_out, k_out
 
@@ -956,7 +957,7 @@ def qk_norm_rope_quantize(q: torch.Tensor, k: torch.Tensor = None, q_weight: tor
         if k_out is None:
             k_out = alloc_qtensor(fmt, k.shape[0] * k.shape[1], d, CANONICAL, k.device)
         kc, ks, _ = _addresses(k_out, fmt, CANONICAL, k.shape[0] * k.shape[1], 0, d, index, "k_out")
-    _ok(_lib.mxq_qk_norm_rope_quantize(h, fmt, hadamard_b, qc, qs, kc, ks, _raw_stream()), "mxq_qk_norm_rope_quantize")
+    _ok(_lib.mxq_qk_norm_rope_quantize(h, fmt, hadamard_b, qc, qs, kc, ks, _stream_handle(index)), "mxq_qk_norm_rope_quantize")
     return q_out, (k_out if k is not None else None)
 
 

@@ -100,11 +100,15 @@ __global__ void __launch_bounds__(kPlanThreads)
         total = own;
         if (counts) {
             total = 0;
-#pragma unroll 8
-            for (int b = 0; b < (int)gridDim.x; b++) {
-                const int c = counts[(int64_t)b * n + e];
-                if (b == (int)blockIdx.x) before = total;
-                total += c;
+            for (int b0 = 0; b0 < (int)gridDim.x; b0 += 32) {   // 32 loads in flight: their latency is this kernel's time
+                int c[32];
+#pragma unroll
+                for (int j = 0; j < 32; j++) c[j] = b0 + j < (int)gridDim.x ? counts[(int64_t)(b0 + j) * n + e] : 0;
+#pragma unroll
+                for (int j = 0; j < 32; j++) {
+                    if (b0 + j == (int)blockIdx.x) before = total;
+                    total += c[j];
+                }
             }
         }
     }
@@ -226,6 +230,18 @@ __device__ __forceinline__ void unpack16(const uint4 (&k)[4], float (&v)[16]) { 
     }
 }
 
+// A chunk as loaded, zeros where there is none.
+template <typename T>
+struct RawWords {
+    uint4 q[sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ void load_words(RawWords<T> &r, const T *p, bool valid) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); i++)
+        r.q[i] = valid ? __ldg(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0, 0, 0, 0);
+}
+
 // max |x| over the tokens that have a row, one maximum per CTA.
 template <typename T>
 __global__ void __launch_bounds__(kGqThreads) k_amax_grouped(const T *__restrict__ x, GroupedQuantArgs a) {
@@ -284,12 +300,24 @@ __global__ void __launch_bounds__(kGqThreads) k_quantize_grouped(const T *__rest
         else rt = recip_of(s);
     }
     const float norm = a.hadamard_b ? __frsqrt_rn((float)a.hadamard_b) : 1.0f;
-    for (uint32_t u = blockIdx.x * kGqWarps + (threadIdx.x >> 5); u < a.units; u += gridDim.x * kGqWarps) {
+    const uint32_t step = gridDim.x * kGqWarps;
+    uint32_t u = blockIdx.x * kGqWarps + (threadIdx.x >> 5);
+    RawWords<T> next;
+    int next_r = -1;
+    auto fetch = [&](uint32_t w) {   // the chunk and the choices of unit w
+        if (w >= a.units) return;
+        const uint32_t t = fdiv(w, a.segs), c = (w - t * a.n_segs) * 32 + lane;
+        load_words(next, x + (int64_t)t * a.cols + (int64_t)c * 16, c < cpr);
+        next_r = choice_row(a, t, lane, first, last);
+    };
+    fetch(u);
+    for (; u < a.units; u += step) {
         const uint32_t t = fdiv(u, a.segs), c = (u - t * a.n_segs) * 32 + lane;
         const bool valid = c < cpr;
         float v[16];
-        load_or_zero(x + (int64_t)t * a.cols + (int64_t)c * 16, valid, v);
-        int r = choice_row(a, t, lane, first, last);
+        unpack16(next.q, v);
+        int r = next_r;
+        fetch(u + step);
         uint32_t sr = 0;
         if (kByte && r >= 0) {   // the row's place among the scales: its group's first tile, then its rank in the group
             const int g = group_of_row(groups, a.n_groups, r);
@@ -432,18 +460,20 @@ __global__ void __launch_bounds__(kGqThreads) k_quantize_grouped_int8(const T *_
 // ------------------------------------------------------------------ combine
 //
 // out[t] = sum over i of weights[t][i] y[slot[t][i]], fp32 FMAs in the order
-// of i.  A thread owns 8 columns of a token and has the rows of four choices
-// in flight at a time.  Bound: HBM.
+// of i.  A warp owns up to 1024 neighbouring columns of a token; lane i reads
+// choice i's row and weight once, and a lane has eight 16-byte loads (four
+// vectors of two rows) in flight.  Bound: HBM.
 
 struct CombineArgs {
-    int64_t rows, n, total;   // total: threads' worth of work
-    FastDiv per_row;          // vectors per token
-    uint32_t n_vec;
+    int64_t rows, n;
+    FastDiv segs;             // warps' worth of columns per token
+    uint32_t n_segs, units, n_vec;   // units = tokens * n_segs; n_vec: vectors per token
     const int32_t *slot;
     const float *weights;
     int topk;
     unsigned int *err;
 };
+constexpr int kCombineSteps = 4;   // vectors of a lane: a warp takes 128 neighbouring ones of a token
 
 template <typename T, int V>
 struct Vec;
@@ -496,37 +526,55 @@ __device__ __forceinline__ void store_vec(float *p, const float (&v)[1]) { *p = 
 
 template <typename T, typename O, int V>
 __global__ void __launch_bounds__(256) k_expert_combine(const T *__restrict__ y, O *__restrict__ out, CombineArgs a) {
+    const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
-    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < a.total; u += (int64_t)gridDim.x * 256) {
-        const uint32_t t = fdiv((uint32_t)u, a.per_row), c = ((uint32_t)u - t * a.n_vec) * V;
-        float acc[V] = {};
-        for (int i0 = 0; i0 < a.topk; i0 += 4) {
-            Vec<T, V> q[4];
-            float w[4];
-            bool on[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int i = i0 + j;
-                const int r = i < a.topk ? a.slot[(int64_t)t * a.topk + i] : -1;
-                on[j] = r >= 0 && r < a.rows;
-                if (r >= a.rows) latch_index_error(a.err);
-                w[j] = 1.0f;
-                if (on[j]) {
-                    if (a.weights) w[j] = a.weights[(int64_t)t * a.topk + i];
-                    q[j].load(y + (int64_t)r * a.n + c);
-                }
+    for (uint32_t u = blockIdx.x * 8 + (threadIdx.x >> 5); u < a.units; u += gridDim.x * 8) {
+        const uint32_t t = fdiv(u, a.segs), c0 = (u - t * a.n_segs) * (32 * kCombineSteps) + lane;
+        int row = -1;   // lane i: choice i's row and weight
+        float weight = 1.0f;
+        if (lane < a.topk) {
+            row = a.slot[(int64_t)t * a.topk + lane];
+            if (a.weights) weight = a.weights[(int64_t)t * a.topk + lane];
+            if (row >= a.rows) {
+                latch_index_error(a.err);
+                row = -1;
             }
+        }
+        unsigned left = __ballot_sync(0xFFFFFFFFu, row >= 0);
+        float acc[kCombineSteps][V] = {};
+        while (left) {   // two rows at a time, all their loads before any use
+            const int i0 = __ffs(left) - 1;
+            left &= left - 1;
+            const int i1 = left ? __ffs(left) - 1 : -1;
+            left &= left - 1;
+            const T *y0 = y + (int64_t)__shfl_sync(0xFFFFFFFFu, row, i0) * a.n;
+            const T *y1 = y + (int64_t)__shfl_sync(0xFFFFFFFFu, row, i1 < 0 ? i0 : i1) * a.n;
+            const float w0 = __shfl_sync(0xFFFFFFFFu, weight, i0), w1 = __shfl_sync(0xFFFFFFFFu, weight, i1 < 0 ? i0 : i1);
+            Vec<T, V> q0[kCombineSteps], q1[kCombineSteps];
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                if (on[j]) {
+            for (int k = 0; k < kCombineSteps; k++)
+                if (c0 + 32 * k < a.n_vec) {
+                    q0[k].load(y0 + (int64_t)(c0 + 32 * k) * V);
+                    if (i1 >= 0) q1[k].load(y1 + (int64_t)(c0 + 32 * k) * V);
+                }
+#pragma unroll
+            for (int k = 0; k < kCombineSteps; k++)
+                if (c0 + 32 * k < a.n_vec) {
                     float v[V];
-                    q[j].get(v);
+                    q0[k].get(v);
 #pragma unroll
-                    for (int k = 0; k < V; k++) acc[k] = __fmaf_rn(w[j], v[k], acc[k]);
+                    for (int j = 0; j < V; j++) acc[k][j] = __fmaf_rn(w0, v[j], acc[k][j]);
+                    if (i1 >= 0) {
+                        q1[k].get(v);
+#pragma unroll
+                        for (int j = 0; j < V; j++) acc[k][j] = __fmaf_rn(w1, v[j], acc[k][j]);
+                    }
                 }
         }
-        store_vec(out + (int64_t)t * a.n + c, acc);
+#pragma unroll
+        for (int k = 0; k < kCombineSteps; k++)
+            if (c0 + 32 * k < a.n_vec) store_vec(out + (int64_t)t * a.n + (int64_t)(c0 + 32 * k) * V, acc[k]);
     }
 }
 
@@ -588,7 +636,7 @@ cudaError_t quantize_grouped(const T *x, int fmt, GroupedQuantArgs a, cudaStream
 
 template <typename T, typename O, int V>
 cudaError_t combine(const void *y, void *out, const CombineArgs &a, cudaStream_t s) {
-    int64_t ctas = (a.total + 255) / 256;
+    int64_t ctas = ((int64_t)a.units + 7) / 8;
     const int64_t cap = (int64_t)sm_count() * 64;
     if (ctas > cap) ctas = cap;
     return launch_pdl(k_expert_combine<T, O, V>, ctas, 256, s, (const T *)y, (O *)out, a);
@@ -644,8 +692,10 @@ cudaError_t launch_expert_combine(const void *y, bool y_bf16, int64_t rows, int6
     const int64_t per_row = vec ? n / 8 : n;
     a.rows = rows;
     a.n = n;
-    a.total = tokens * per_row;
-    a.per_row = make_fastdiv((uint32_t)per_row);
+    const int64_t segs = (per_row + 32 * kCombineSteps - 1) / (32 * kCombineSteps);
+    a.segs = make_fastdiv((uint32_t)segs);
+    a.n_segs = (uint32_t)segs;
+    a.units = (uint32_t)(tokens * segs);
     a.n_vec = (uint32_t)per_row;
     a.slot = slot;
     a.weights = weights;

@@ -11,11 +11,14 @@
 // weight.  Per CTA:
 //   warp 0      TMA producer into a 5-stage ring: 128 weight rows x 128 bytes,
 //               16 / 32 / 64 / 128 rows of X by the box that fits, scale atoms
-//   warp 1      TMEM allocation and the thread that copies a stage's scale
-//               atoms to TMEM (tcgen05.cp, each stage its own columns) and
-//               issues its MMAs
+//   warp 1      TMEM allocation and the thread that issues the MMAs
 //   warps 2-5   epilogue: TMEM -> shared staging [32 rows][128 features] ->
 //               scaled rows of y
+//   warps 6-    a thread per scale atom of a stage that copies it (X's and
+//               W's) to TMEM, each stage having its own columns: a tcgen05.cp
+//               holds up the thread that issues it, and NVFP4 has eight a
+//               stage (one token, 8 of 64 experts, 2048 x 4096: 15.1 us with
+//               the MMA thread issuing them)
 // The kernel is persistent over items (expert, 128 features, 128 rows); an
 // expert's row blocks of one weight tile are neighbours, so the weight's
 // second read is served by L2.  Two accumulator stages let an item's loads and
@@ -47,7 +50,6 @@ constexpr int GN_SF = 2048;            // up to 4 scale atoms of 512 bytes, for 
 constexpr int GN_STAGE = GN_W + GN_X + 2 * GN_SF;
 constexpr int GN_STAGING = 32 * 128 * 4;
 constexpr int GN_SMEM = GN_STAGES * GN_STAGE + GN_STAGING + (int)sizeof(Groups) + 256 + 1024;
-constexpr int GN_THREADS = 192;
 constexpr uint32_t GN_TMEM_COLS = 512;
 constexpr uint32_t GN_TMEM_SF = 256;   // two 128-column accumulators, then 32 columns of scales per stage
 static_assert(GN_TMEM_SF + 32 * GN_STAGES <= GN_TMEM_COLS, "TMEM budget");
@@ -96,6 +98,8 @@ __device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;
 
 template <int F>
 __host__ __device__ constexpr int gn_atoms() { return F == kNVFP4 ? 4 : F == kMXFP4 ? 2 : F == kMXFP8 ? 1 : 0; }
+template <int F>
+__host__ __device__ constexpr int gn_threads() { return 192 + 32 * gn_atoms<F>(); }
 template <int F>
 __host__ __device__ constexpr uint32_t gn_idesc() {   // M = 128, K-major operands; N is or-ed in
     return (8u << 24) | (F == kNVFP4   ? (1u << 7) | (1u << 10)                 // E2M1, UE4M3 scales
@@ -162,7 +166,7 @@ __device__ __forceinline__ Item item_at(const Groups &g, int n_groups, int n_til
 }
 
 template <int F>
-__global__ void __launch_bounds__(GN_THREADS, 1) k_gemm_grouped_few(const __grid_constant__ GroupedParams p) {
+__global__ void __launch_bounds__(gn_threads<F>(), 1) k_gemm_grouped_few(const __grid_constant__ GroupedParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint32_t *staging = reinterpret_cast<uint32_t *>(smem + GN_STAGES * GN_STAGE);
@@ -173,7 +177,8 @@ __global__ void __launch_bounds__(GN_THREADS, 1) k_gemm_grouped_few(const __grid
     uint64_t *ready = acce + 2;           // partial sums of every CTA of the cluster in its staging
     uint64_t *freed = ready + 1;          // and read by all of them
     uint64_t *drain = freed + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *sfready = drain + 1;        // [GN_STAGES] a stage's scales in TMEM
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sfready + GN_STAGES);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Groups &groups = *reinterpret_cast<Groups *>(smem + GN_STAGES * GN_STAGE + GN_STAGING + 256);
 
@@ -184,10 +189,15 @@ __global__ void __launch_bounds__(GN_THREADS, 1) k_gemm_grouped_few(const __grid
     const int cid = (int)cluster_id(), ncl = (int)cluster_count();
     constexpr int NSF = gn_atoms<F>();
 
+    if (warp == 0 && lane < 7) {
+        const CUtensorMap *m = lane < 4 ? p.x + lane : lane == 4 ? &p.w : lane == 5 ? &p.sfw : &p.sfx;
+        if (lane < 5 || NSF) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < GN_STAGES; s++) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
+            mbar_init(sfready + s, NSF ? NSF : 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(accf + i, 1);
@@ -195,7 +205,7 @@ __global__ void __launch_bounds__(GN_THREADS, 1) k_gemm_grouped_few(const __grid
         }
         mbar_init(ready, 4 * split);
         mbar_init(freed, 4 * split);
-        mbar_init(drain, 1);
+        mbar_init(drain, 1 + NSF);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -249,7 +259,6 @@ __global__ void __launch_bounds__(GN_THREADS, 1) k_gemm_grouped_few(const __grid
         if (lane == 0) {
             int it = 0, count = 0;
             const uint64_t ad0 = sdesc_sw128(smem), bd0 = sdesc_sw128(smem + GN_W);
-            bool issued = false;
             for (int item = cid; item < items && !*abort_flag; item += ncl, count++) {
                 const Item w = item_at(groups, p.n_groups, p.n_tiles, item);
                 const uint32_t idesc = gn_idesc<F>() | ((uint32_t)((w.n_rows + 15) >> 4) << 18);   // N / 8 at bit 17
@@ -259,19 +268,12 @@ __global__ void __launch_bounds__(GN_THREADS, 1) k_gemm_grouped_few(const __grid
                 tc_fence_after();
                 for (int kt = kt0; kt < kt1 && ok && !*abort_flag; kt++, it++) {
                     const int s = it % GN_STAGES;
-                    ok = mbar_wait_spin(full + s, (it / GN_STAGES) & 1, p.wait_ns);
+                    ok = mbar_wait_spin(NSF ? sfready + s : full + s, (it / GN_STAGES) & 1, p.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint8_t *sf = smem + s * GN_STAGE + GN_W + GN_X;
                     const uint32_t sft = tmem + GN_TMEM_SF + 32u * s;
                     const int left = (p.kbytes - kt * 128) >> 5, nks = left < 4 ? left : 4;
                     const uint64_t off = (uint64_t)(s * (GN_STAGE >> 4));
-                    issued = true;
-#pragma unroll
-                    for (int i = 0; i < NSF; i++) {   // copies and MMAs of one thread run in order
-                        tc_cp(sft + 8 * i, sdesc_atom(sf + 512 * i));
-                        tc_cp(sft + 8 * i + 4, sdesc_atom(sf + GN_SF + 512 * i));
-                    }
 #pragma unroll
                     for (int ks = 0; ks < 4; ks++)
                         if (ks < nks)
@@ -285,7 +287,35 @@ __global__ void __launch_bounds__(GN_THREADS, 1) k_gemm_grouped_few(const __grid
                 if (*abort_flag) break;
                 tc_commit(accf + st);
             }
-            if (*abort_flag && issued) {
+            if (*abort_flag) {   // what is in flight lands before the TMEM is freed
+                tc_commit(drain);
+                mbar_wait(drain, 0, p.wait_ns);
+            }
+        }
+    } else if (warp >= 6) {
+        const int atom = warp - 6;
+        if (lane == 0) {
+            int it = 0;
+            for (int item = cid; item < items && !*abort_flag; item += ncl) {
+                for (int kt = kt0; kt < kt1; kt++, it++) {
+                    const int s = it % GN_STAGES;
+                    if (!mbar_wait(full + s, (it / GN_STAGES) & 1, p.wait_ns)) {
+                        atomicOr(p.err, kErrGrouped);
+                        *abort_flag = 1;
+                    }
+                    if (*abort_flag) break;
+                    tc_fence_after();
+                    // atoms of 32-byte k-steps: 4 (NVFP4: one each), 2 or 1 a stage, fewer in the last
+                    if (atom * (4 / (NSF ? NSF : 1)) * 32 < p.kbytes - kt * 128) {
+                        const uint8_t *sf = smem + s * GN_STAGE + GN_W + GN_X + 512 * atom;
+                        const uint32_t to = tmem + GN_TMEM_SF + 32u * s + 8u * atom;
+                        tc_cp(to, sdesc_atom(sf));
+                        tc_cp(to + 4, sdesc_atom(sf + GN_SF));
+                    }
+                    tc_commit(sfready + s);
+                }
+            }
+            if (*abort_flag) {
                 tc_commit(drain);
                 mbar_wait(drain, 0, p.wait_ns);
             }
@@ -435,7 +465,7 @@ cudaError_t launch_few(const GroupedParams &p, int clusters, int split, cudaStre
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * split), 1, 1);
-    cfg.blockDim = dim3(GN_THREADS, 1, 1);
+    cfg.blockDim = dim3(gn_threads<F>(), 1, 1);
     cfg.dynamicSmemBytes = GN_SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[2] = {pdl_attribute()};
@@ -505,7 +535,7 @@ static cudaError_t launch_qlinear_grouped_few(const GroupedOperands &op, cudaStr
 // The host knows the rows of all experts together, not of each: their mean
 // decides.
 cudaError_t launch_qlinear_grouped(const GroupedOperands &op, cudaStream_t s) {
-    if (op.rows > 128 * (int64_t)op.n_groups) return launch_qlinear_grouped_many(op, s);
+    if (op.rows > 64 * (int64_t)op.n_groups) return launch_qlinear_grouped_many(op, s);
     return launch_qlinear_grouped_few(op, s);
 }
 
