@@ -649,7 +649,7 @@ mxq_status mxq_expert_plan_workspace_bytes(int64_t rows, int32_t n_experts, size
  *   expert_ids: device, id_bits = 32 or 64 bit integers, rows of them (token
  *     by token); ids outside [0, n_experts) are dropped choices.
  *   offsets: device int32[n_experts + 1]; slot: device int32[rows].
- *   workspace: device scratch of mxq_expert_plan_workspace_bytes (may be NULL
+ *   workspace: device scratch of mxq_expert_plan_workspace_bytes, 16-byte aligned (may be NULL
  *     when that is 0); clobbered.
  * The same ids give the same plan, bit for bit.
  * Errors: MXQ_EINVAL (sizes, pointers, alignment), MXQ_ENOSPACE, MXQ_ECUDA. */

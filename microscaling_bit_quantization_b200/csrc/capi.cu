@@ -871,7 +871,7 @@ mxq_status mxq_expert_plan(const void *expert_ids, int32_t id_bits, int64_t rows
                      (reinterpret_cast<uintptr_t>(expert_ids) & (uintptr_t)(id_bits / 8 - 1)) != 0))
         return MXQ_EINVAL;
     const size_t need = plan_workspace_bytes(rows, n_experts);
-    if (need && (!workspace || !aligned4(workspace))) return MXQ_EINVAL;
+    if (need && (!workspace || !aligned16(workspace))) return MXQ_EINVAL;
     if (workspace_bytes < need) return MXQ_ENOSPACE;
     return from_cuda(launch_expert_plan(expert_ids, id_bits == 64, rows, n_experts, offsets, slot, (int32_t *)workspace,
                                         (cudaStream_t)stream));

@@ -43,6 +43,9 @@ __device__ __forceinline__ int expert_at(const I *ids, int64_t i, int64_t end, i
     return v >= 0 && v < (I)n ? (int)v : -1;
 }
 
+// Counts of a block lie plan_stride(n) apart: whole 16-byte words.
+__host__ __device__ __forceinline__ int plan_stride(int n) { return (n + 3) & ~3; }
+
 template <typename I>
 __global__ void __launch_bounds__(kPlanThreads) k_plan_count(const I *__restrict__ ids, int64_t rows, int n,
                                                              int64_t per_block, int32_t *__restrict__ counts) {
@@ -62,7 +65,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_count(const I *__restrict
             if (e[j] >= 0) atomicAdd(hist + e[j], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < n; e += kPlanThreads) counts[(int64_t)blockIdx.x * n + e] = hist[e];
+    const int stride = plan_stride(n);
+    for (int e = threadIdx.x; e < stride; e += kPlanThreads) counts[(int64_t)blockIdx.x * stride + e] = e < n ? hist[e] : 0;
 }
 
 // counts: null with one block, else k_plan_count's.
@@ -72,10 +76,14 @@ __global__ void __launch_bounds__(kPlanThreads)
                  int32_t *__restrict__ offsets, int32_t *__restrict__ slot) {
     __shared__ int at[kPlanWarps][kMaxGroups];   // counts, then the next row, of each warp's choices of each expert
     __shared__ int warp_sum[kPlanWarps];
+    __shared__ int all[kMaxGroups], earlier[kMaxGroups];   // choices of each expert in all blocks, and in those before this
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_wait();
+    // k_plan_count is the kernel before this one and lets it start only once
+    // it has itself waited for the ids: they may be read before the wait
+    if (!counts) pdl_wait();
     pdl_launch_dependents();
     for (int i = threadIdx.x; i < kPlanWarps * kMaxGroups; i += kPlanThreads) (&at[0][0])[i] = 0;
+    all[threadIdx.x] = earlier[threadIdx.x] = 0;
     __syncthreads();
     const int64_t begin = (int64_t)blockIdx.x * per_block;
     const int64_t end = begin + per_block < rows ? begin + per_block : rows;
@@ -83,13 +91,43 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int64_t per_warp = ((end - begin + kPlanThreads - 1) / kPlanThreads) * 32;
     const int64_t w_begin = begin + warp * per_warp;
     const int64_t w_end = w_begin + per_warp < end ? w_begin + per_warp : end;
+    int keep[4] = {-1, -1, -1, -1};   // the first 128 choices, for the second walk
     for (int64_t i0 = w_begin; i0 < w_end; i0 += 128) {
         int e[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) e[j] = expert_at(ids, i0 + 32 * j + lane, w_end, n);
 #pragma unroll
-        for (int j = 0; j < 4; j++)
+        for (int j = 0; j < 4; j++) {
             if (e[j] >= 0) atomicAdd(&at[warp][e[j]], 1);   // a count: no order in it
+            if (i0 == w_begin) keep[j] = e[j];
+        }
+    }
+    if (counts) {
+        pdl_wait();
+        // a thread adds four experts' counts over every rows-th block, its loads eight at a time
+        const int stride = plan_stride(n), groups = stride / 4, rows_of = kPlanThreads / groups;
+        const int g = threadIdx.x % groups, start = threadIdx.x / groups, nb = (int)gridDim.x;
+        int4 sum = make_int4(0, 0, 0, 0), pre = sum;
+        if (start < rows_of) {
+            for (int b0 = start; b0 < nb; b0 += 8 * rows_of) {
+                int4 c[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const int b = b0 + j * rows_of;
+                    c[j] = __ldcg(reinterpret_cast<const int4 *>(counts + (int64_t)(b < nb ? b : 0) * stride) + g);
+                    if (b >= nb) c[j] = make_int4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    sum.x += c[j].x, sum.y += c[j].y, sum.z += c[j].z, sum.w += c[j].w;
+                    if (b0 + j * rows_of < (int)blockIdx.x) pre.x += c[j].x, pre.y += c[j].y, pre.z += c[j].z, pre.w += c[j].w;
+                }
+            }
+            atomicAdd(all + 4 * g, sum.x), atomicAdd(all + 4 * g + 1, sum.y);
+            atomicAdd(all + 4 * g + 2, sum.z), atomicAdd(all + 4 * g + 3, sum.w);
+            atomicAdd(earlier + 4 * g, pre.x), atomicAdd(earlier + 4 * g + 1, pre.y);
+            atomicAdd(earlier + 4 * g + 2, pre.z), atomicAdd(earlier + 4 * g + 3, pre.w);
+        }
     }
     __syncthreads();
     int own = 0, before = 0, total = 0;
@@ -99,17 +137,8 @@ __global__ void __launch_bounds__(kPlanThreads)
         for (int w = 0; w < kPlanWarps; w++) own += at[w][e];
         total = own;
         if (counts) {
-            total = 0;
-            for (int b0 = 0; b0 < (int)gridDim.x; b0 += 32) {   // 32 loads in flight: their latency is this kernel's time
-                int c[32];
-#pragma unroll
-                for (int j = 0; j < 32; j++) c[j] = b0 + j < (int)gridDim.x ? counts[(int64_t)(b0 + j) * n + e] : 0;
-#pragma unroll
-                for (int j = 0; j < 32; j++) {
-                    if (b0 + j == (int)blockIdx.x) before = total;
-                    total += c[j];
-                }
-            }
+            total = all[e];
+            before = earlier[e];
         }
     }
     // exclusive scan of the totals over the experts
@@ -141,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int64_t i0 = w_begin; i0 < w_end; i0 += 128) {
         int ex[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) ex[j] = expert_at(ids, i0 + 32 * j + lane, w_end, n);
+        for (int j = 0; j < 4; j++) ex[j] = i0 == w_begin ? keep[j] : expert_at(ids, i0 + 32 * j + lane, w_end, n);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             const unsigned same = __match_any_sync(0xFFFFFFFFu, ex[j]);
@@ -646,7 +675,7 @@ cudaError_t combine(const void *y, void *out, const CombineArgs &a, cudaStream_t
 
 size_t plan_workspace_bytes(int64_t rows, int n_experts) {
     const int nb = plan_blocks(rows);
-    return nb > 1 ? (size_t)nb * n_experts * 4 : 0;
+    return nb > 1 ? (size_t)nb * plan_stride(n_experts) * 4 : 0;
 }
 
 cudaError_t launch_expert_plan(const void *ids, bool ids64, int64_t rows, int n_experts, int32_t *offsets, int32_t *slot,
