@@ -189,21 +189,23 @@ __global__ void __launch_bounds__(kPlanThreads)
 //
 // A token is read and coded once and its codes written to the rows of all
 // its choices: T K reads and T k K writes, against k times the reads of a
-// gather.  A warp takes 32 consecutive 16-element chunks of a token (the
-// chunk mapping of k_quantize, so blocks and Hadamard blocks lie in aligned
-// lanes), and lane i looks up choice i's row and its place in the grouped
-// scale layout while the chunk's load is in flight.  Four block scales are
-// gathered into the 4-byte word they share in a scale atom.
-// Bound: HBM.
+// gather.  A warp takes up to four spans of 32 consecutive 16-element chunks
+// of a token (the chunk mapping of k_quantize, so blocks and Hadamard blocks
+// lie in aligned lanes); lane i looks up choice i's row and its place in the
+// grouped scale layout once for all of them, and the next span's load is in
+// flight while one is coded.  Four block scales are gathered into the 4-byte
+// word they share in a scale atom.  Bound: HBM.
 
 constexpr int kGqThreads = 256;
 constexpr int kGqWarps = kGqThreads / 32;
+constexpr uint32_t kGqSpans = 4;
 constexpr int kGqMaxCtas = 960;   // per-CTA maxima of the tensor-amax pass
 
 struct GroupedQuantArgs {
     int64_t x_rows, cols, rows;   // rows: capacity of codes and scales
-    FastDiv segs;                 // warps' worth of chunks per token
+    FastDiv segs;                 // warps' work per token
     uint32_t n_segs, units;       // units = x_rows * n_segs
+    uint32_t spans;               // spans of 32 chunks that a unit holds at most
     const int32_t *slot;          // null: token t is row t
     int topk;
     const int32_t *offsets;
@@ -283,13 +285,18 @@ __global__ void __launch_bounds__(kGqThreads) k_amax_grouped(const T *__restrict
     const uint32_t cpr = (uint32_t)(a.cols >> 4);
     float m = 0.0f;
     for (uint32_t u = blockIdx.x * kGqWarps + (threadIdx.x >> 5); u < a.units; u += gridDim.x * kGqWarps) {
-        const uint32_t t = fdiv(u, a.segs), c = (u - t * a.n_segs) * 32 + lane;
-        float v[16];
-        load_or_zero(x + (int64_t)t * a.cols + (int64_t)c * 16, c < cpr, v);
+        const uint32_t t = fdiv(u, a.segs), c0 = (u - t * a.n_segs) * a.spans * 32 + lane;
         const int r = choice_row(a, t, lane, first, last);
         if (!__any_sync(0xFFFFFFFFu, r >= 0)) continue;
-        if (a.hadamard_b) hadamard_chunk_n(v, a.hadamard_b, lane, norm);
-        m = fmaxf(m, amax16(v));
+#pragma unroll
+        for (uint32_t j = 0; j < kGqSpans; j++) {
+            if (j >= a.spans) break;
+            const uint32_t c = c0 + 32 * j;
+            float v[16];
+            load_or_zero(x + (int64_t)t * a.cols + (int64_t)c * 16, c < cpr, v);
+            if (a.hadamard_b) hadamard_chunk_n(v, a.hadamard_b, lane, norm);
+            m = fmaxf(m, amax16(v));
+        }
     }
     m = group_max<32>(m);
     if (lane == 0) wm[threadIdx.x >> 5] = m;
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__(kGqThreads) k_amax_grouped(const T *__restrict
 
 // Formats with byte scales, and FP8 per tensor.
 template <typename T, int F>
-__global__ void __launch_bounds__(kGqThreads) k_quantize_grouped(const T *__restrict__ x, GroupedQuantArgs a) {
+__global__ void __launch_bounds__(kGqThreads, 4) k_quantize_grouped(const T *__restrict__ x, GroupedQuantArgs a) {
     __shared__ Groups groups;
     __shared__ float wm[kGqWarps];
     const int lane = threadIdx.x & 31;
@@ -329,32 +336,58 @@ __global__ void __launch_bounds__(kGqThreads) k_quantize_grouped(const T *__rest
         else rt = recip_of(s);
     }
     const float norm = a.hadamard_b ? __frsqrt_rn((float)a.hadamard_b) : 1.0f;
-    const uint32_t step = gridDim.x * kGqWarps;
+    const uint32_t step = gridDim.x * kGqWarps, spans_t = (cpr + 31) >> 5;
     uint32_t u = blockIdx.x * kGqWarps + (threadIdx.x >> 5);
-    RawWords<T> next;
-    int next_r = -1;
-    auto fetch = [&](uint32_t w) {   // the chunk and the choices of unit w
-        if (w >= a.units) return;
-        const uint32_t t = fdiv(w, a.segs), c = (w - t * a.n_segs) * 32 + lane;
-        load_words(next, x + (int64_t)t * a.cols + (int64_t)c * 16, c < cpr);
-        next_r = choice_row(a, t, lane, first, last);
+    if (u >= a.units) return;
+    // the span being coded: token t, chunk c of this lane, `left` more spans in the unit
+    uint32_t t, c, left;
+    auto unit = [&](uint32_t w, uint32_t &wt, uint32_t &wc, uint32_t &wleft) {
+        wt = fdiv(w, a.segs);
+        const uint32_t s0 = (w - wt * a.n_segs) * a.spans;
+        wc = s0 * 32 + lane;
+        wleft = (spans_t - s0 < a.spans ? spans_t - s0 : a.spans) - 1;
     };
-    fetch(u);
-    for (; u < a.units; u += step) {
-        const uint32_t t = fdiv(u, a.segs), c = (u - t * a.n_segs) * 32 + lane;
+    unit(u, t, c, left);
+    RawWords<T> next;
+    load_words(next, x + (int64_t)t * a.cols + (int64_t)c * 16, c < cpr);
+    int next_r = choice_row(a, t, lane, first, last), r = -1;
+    uint32_t sword = 0;      // lane i: the row's first word among the scales
+    unsigned any = 0;
+    bool fresh = true;       // a new token: look its choices up
+    while (true) {
         const bool valid = c < cpr;
+        const uint32_t cur = c;
         float v[16];
         unpack16(next.q, v);
-        int r = next_r;
-        fetch(u + step);
-        uint32_t sr = 0;
-        if (kByte && r >= 0) {   // the row's place among the scales: its group's first tile, then its rank in the group
-            const int g = group_of_row(groups, a.n_groups, r);
-            if (g >= 0) sr = (uint32_t)(128 * groups.tile[g] + r - groups.off[g]);
-            if (g < 0 || (sr >> 7) >= a.scale_tiles) r = -1;   // offsets that do not fit the buffers
+        if (fresh) {
+            r = next_r;
+            if (kByte && r >= 0) {   // its group's first tile, then its rank in the group
+                const int g = group_of_row(groups, a.n_groups, r);
+                const uint32_t sr = g >= 0 ? (uint32_t)(128 * groups.tile[g] + r - groups.off[g]) : 0u;
+                if (g < 0 || (sr >> 7) >= a.scale_tiles) r = -1;   // offsets that do not fit the buffers
+                sword = (sr >> 7) * a.s_pad4 * 128 + (sr & 31) * 4 + ((sr >> 5) & 3);
+            }
+            any = __ballot_sync(0xFFFFFFFFu, r >= 0);
         }
-        const unsigned any = __ballot_sync(0xFFFFFFFFu, r >= 0);
-        if (!any) continue;
+        // the next span's load
+        fresh = left == 0;
+        bool more = true;
+        if (!fresh) {
+            c += 32;
+            left--;
+        } else {
+            u += step;
+            more = u < a.units;
+            if (more) {
+                unit(u, t, c, left);
+                next_r = choice_row(a, t, lane, first, last);
+            }
+        }
+        if (more) load_words(next, x + (int64_t)t * a.cols + (int64_t)c * 16, c < cpr);
+        if (!any) {
+            if (!more) break;
+            continue;
+        }
         if (a.hadamard_b) hadamard_chunk_n(v, a.hadamard_b, lane, norm);
         uint32_t w[4];        // codes: 16 bytes (8-bit elements) or 8
         uint32_t scale = 0;   // this lane's block scale
@@ -398,20 +431,22 @@ __global__ void __launch_bounds__(kGqThreads) k_quantize_grouped(const T *__rest
                    (__shfl_down_sync(0xFFFFFFFFu, scale, 2 * L) << 16) |
                    (__shfl_down_sync(0xFFFFFFFFu, scale, 3 * L) << 24);
             leader = valid && (lane & (4 * L - 1)) == 0;
-            col = c / L;
+            col = cur / L;
         }
-        for (unsigned left = any; left; left &= left - 1) {
-            const int i = __ffs(left) - 1;
+        uint8_t *codes = a.codes + (int64_t)cur * (fmt_is4(F) ? 8 : 16);
+        uint32_t *scales = reinterpret_cast<uint32_t *>(a.scales) + (col >> 2) * 128u;
+        const int64_t pitch = (int64_t)cpr * (fmt_is4(F) ? 8 : 16);
+        for (unsigned rest = any; rest; rest &= rest - 1) {
+            const int i = __ffs(rest) - 1;
             const int row = __shfl_sync(0xFFFFFFFFu, r, i);
-            const uint32_t srow = kByte ? __shfl_sync(0xFFFFFFFFu, sr, i) : 0u;
-            const int64_t chunk = (int64_t)row * cpr + c;
+            const uint32_t word_at = kByte ? __shfl_sync(0xFFFFFFFFu, sword, i) : 0u;
             if (valid) {
-                if (fmt_is4(F)) *reinterpret_cast<uint2 *>(a.codes + chunk * 8) = make_uint2(w[0], w[1]);
-                else *reinterpret_cast<uint4 *>(a.codes + chunk * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (fmt_is4(F)) *reinterpret_cast<uint2 *>(codes + row * pitch) = make_uint2(w[0], w[1]);
+                else *reinterpret_cast<uint4 *>(codes + row * pitch) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (kByte && leader)
-                *reinterpret_cast<uint32_t *>(a.scales + mma_scale_offset(srow, col, (int64_t)a.s_pad4 * 4)) = word;
+            if (kByte && leader) scales[word_at] = word;
         }
+        if (!more) break;
     }
 }
 
@@ -688,7 +723,10 @@ cudaError_t launch_quantize_grouped(const void *x, bool bf16, int64_t x_rows, in
                                     const int32_t *offsets, int n_groups, const int32_t *slot, int topk, int64_t rows,
                                     void *codes, void *scales, float *tensor_scale, float *amax_slots, cudaStream_t s) {
     GroupedQuantArgs a = {};
-    const int64_t segs = (cols / 16 + 31) / 32;
+    // a warp takes four spans of a token where that still gives every SM 32 warps, else one
+    const int64_t spans_t = (cols / 16 + 31) / 32;
+    a.spans = x_rows * ((spans_t + kGqSpans - 1) / kGqSpans) >= (int64_t)sm_count() * 32 ? kGqSpans : 1;
+    const int64_t segs = (spans_t + a.spans - 1) / a.spans;
     a.x_rows = x_rows;
     a.cols = cols;
     a.rows = rows;
