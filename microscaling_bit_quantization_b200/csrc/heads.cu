@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope(HeadKernelArgs a)
     const int64_t total = h.tokens * a.items;
     for (int64_t it = (int64_t)blockIdx.x * kHeadWarps + (threadIdx.x >> 5); it < total;
          it += (int64_t)gridDim.x * kHeadWarps) {
-        const int64_t t = it / a.items;
+        const int64_t t = a.items == 1 ? it : it / a.items;
         const int pass0 = (int)(it - t * a.items) * a.per_item;
         const int pass1 = pass0 + a.per_item < a.passes ? pass0 + a.per_item : a.passes;
         // head i of the token at qx + i d, or kx + i d for the k heads
@@ -305,146 +305,168 @@ __global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope(HeadKernelArgs a)
     }
 }
 
+// Block-diagonal Hadamard rotation of the heads in a pass without its factor
+// 1/sqrt(b): lane u of a head holds its elements 8u .. 8u + 7, the even ones in
+// v.a and the odd ones in v.b.  Stages 1, 2 and 4 lie in the lane, stage 8 l
+// pairs lanes that differ in bit l: a lane's elements stay or change sign and
+// the partner's are added, one packed FMA for two.
+template <int UNITS>
+__device__ __forceinline__ void hadamard_heads(Pairs &v, int b, int lane) {
+    const float2 minus = make_float2(-1.0f, -1.0f);
+    auto both = [&](float2 &x, float2 &y) {   // (x + y, x - y)
+        const float2 s = __fadd2_rn(x, y);
+        y = fma2(y, minus, x);
+        x = s;
+    };
+    both(v.a[0], v.b[0]);
+    both(v.a[1], v.b[1]);
+    if (b > 2) {
+        auto inside = [](float2 &x) { x = make_float2(__fadd_rn(x.x, x.y), __fsub_rn(x.x, x.y)); };
+        inside(v.a[0]);
+        inside(v.a[1]);
+        inside(v.b[0]);
+        inside(v.b[1]);
+    }
+    if (b > 4) {
+        both(v.a[0], v.a[1]);
+        both(v.b[0], v.b[1]);
+    }
+#pragma unroll
+    for (int l = 1; l < (UNITS ? UNITS : 32); l <<= 1) {
+        if (8 * l < b) {
+            const float sign = (lane & l) ? -1.0f : 1.0f;
+            const float2 sg = make_float2(sign, sign);
+            auto cross = [&](float2 &x) {
+                x = fma2(sg, x, make_float2(__shfl_xor_sync(0xFFFFFFFFu, x.x, l), __shfl_xor_sync(0xFFFFFFFFu, x.y, l)));
+            };
+            cross(v.a[0]);
+            cross(v.a[1]);
+            cross(v.b[0]);
+            cross(v.b[1]);
+        }
+    }
+}
+
 // The same, then an optional Hadamard rotation and the codes of every head.
-// Two passes' heads go through shared memory (fp32, in rows of 16 elements
-// and 4 of padding, which spreads a warp's 16-byte accesses over the banks)
-// to the 16-element chunks of the quantizers, one chunk per lane, so that a
-// quantization or Hadamard block lies in aligned neighbouring lanes.  The
-// head's factor and 1/sqrt(b) are applied where the codes are formed.
+// Codes want a lane to hold 8 neighbouring elements.  Interleaved pairs have
+// them so; pairs of halves go through shared memory (1 KB per warp), stored so
+// that both 16-byte reads give even and odd elements apart.  The head's factor
+// and 1/sqrt(b) are applied where the codes are formed.  Bound: instruction
+// issue, most of it the rotation's 8 exchanges per stage.
 template <typename T, int F, int UNITS, bool IL>
-__global__ void __launch_bounds__(kHeadThreads, 5) k_qk_norm_rope_quantize(HeadKernelArgs a) {
-    __shared__ __align__(16) float buf[kHeadWarps][32 * 20];
-    __shared__ float factor[kHeadWarps][64];
+__global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope_quantize(HeadKernelArgs a) {
+    __shared__ __align__(16) float buf[IL ? 1 : kHeadWarps][IL ? 4 : 256];
     const HeadArgs &h = a.h;
     const int lane = threadIdx.x & 31;
-    float *b = buf[threadIdx.x >> 5], *fac = factor[threadIdx.x >> 5];
+    float *b = buf[IL ? 0 : threadIdx.x >> 5];
     const LanePlace<UNITS, IL> q(a, lane);
     const int heads = h.q_heads + h.k_heads, d = h.head_dim;
-    const int chunks = UNITS ? UNITS / 2 : d / 16;                                  // lanes per head when coding
-    const int chead = lane / chunks, cc = lane - chead * chunks;                    // head of the two passes', chunk of it
     const float norm = h.hadamard_b ? __frsqrt_rn((float)h.hadamard_b) : 1.0f;
-    auto padded = [](int e) { return (e >> 4) * 20 + (e & 15); };
-    float *b0 = b + padded(q.sub * d + q.p0), *b1 = b + padded(q.sub * d + q.p1);   // this lane's elements, first pass
-    const int second = padded(a.per_pass * d);                                      // (per_pass d is a multiple of 32)
     pdl_wait();
     pdl_launch_dependents();
     const int64_t total = h.tokens * a.items;
     for (int64_t it = (int64_t)blockIdx.x * kHeadWarps + (threadIdx.x >> 5); it < total;
          it += (int64_t)gridDim.x * kHeadWarps) {
-        const int64_t t = it / a.items;
+        const int64_t t = a.items == 1 ? it : it / a.items;
         const int pass0 = (int)(it - t * a.items) * a.per_item;
         const int pass1 = pass0 + a.per_item < a.passes ? pass0 + a.per_item : a.passes;
         const T *qx = (const T *)h.q + t * h.q_stride, *kx = (const T *)h.k + t * h.k_stride - (int64_t)h.q_heads * d;
         const int end = pass1 * a.per_pass < heads ? pass1 * a.per_pass : heads;
         const int64_t qrow = t * h.q_heads, krow = t * h.k_heads - h.q_heads;   // row of head i: qrow + i or krow + i
         int head = q.in_pass ? pass0 * a.per_pass + q.sub : end;
-        Raw<T> next[2] = {};
-        auto load = [&](int i, Raw<T> &r) {
-            if (i < end) load_raw<IL>(r, (i < h.q_heads ? qx : kx) + (int64_t)i * d, q.p0, q.p1);
-        };
-        load(head, next[0]);
-        load(head + a.per_pass, next[1]);
+        Raw<T> next = {};
+        if (head < end) load_raw<IL>(next, (head < h.q_heads ? qx : kx) + (int64_t)head * d, q.p0, q.p1);
         const int64_t pos = position_of(h, t, a.err);
         Turn turn = {};
         int side = -1;
-        for (int pass = pass0; pass < pass1; pass += 2) {
-            Pairs v[2] = {unpack<IL>(next[0]), unpack<IL>(next[1])};
-            load(head + 2 * a.per_pass, next[0]);
-            load(head + 3 * a.per_pass, next[1]);
-            __syncwarp();   // the chunks of the passes before have been read
-#pragma unroll
-            for (int p = 0; p < 2; p++) {
-                const int is_k = head >= h.q_heads;
-                if (is_k != side && head < end) {
-                    side = is_k;
-                    turn = turn_of<IL>(h, is_k ? h.k_weight : h.q_weight, q.u, q.p0, q.p1, q.turned, pos < 0 ? 0 : pos);
-                }
-                const float r = norm_turn<UNITS>(v[p], h, turn, q.turned, q.u, a.units, lane);
+        for (int pass = pass0; pass < pass1; pass++) {
+            Pairs v = unpack<IL>(next);
+            const int now = head;
+            const bool valid = now < end;
+            head += a.per_pass;
+            if (head < end) load_raw<IL>(next, (head < h.q_heads ? qx : kx) + (int64_t)head * d, q.p0, q.p1);
+            const int is_k = now >= h.q_heads;
+            if (is_k != side && valid) {
+                side = is_k;
+                turn = turn_of<IL>(h, is_k ? h.k_weight : h.q_weight, q.u, q.p0, q.p1, q.turned, pos < 0 ? 0 : pos);
+            }
+            const float f = norm_turn<UNITS>(v, h, turn, q.turned, q.u, a.units, lane) * norm;
+            if (!IL) {
+                __syncwarp();   // the pass before has been read
                 if (q.in_pass) {
-                    float4 x, y;
-                    in_order<IL>(v[p], x, y);
-                    *reinterpret_cast<float4 *>(b0 + p * second) = x;
-                    *reinterpret_cast<float4 *>(b1 + p * second) = y;
-                    if (q.u == 0) fac[p * a.per_pass + q.sub] = r * norm;
+                    *reinterpret_cast<float4 *>(b + q.sub * d + q.p0) = make_float4(v.a[0].x, v.a[1].x, v.a[0].y, v.a[1].y);
+                    *reinterpret_cast<float4 *>(b + q.sub * d + q.p1) = make_float4(v.b[0].x, v.b[1].x, v.b[0].y, v.b[1].y);
                 }
-                head += a.per_pass;
-            }
-            __syncwarp();
-            const int chd = pass * a.per_pass + chead;
-            const bool valid = chead < 2 * a.per_pass && chd < end;
-            float x[16];
-            {
-                const float4 *src = reinterpret_cast<const float4 *>(b + lane * 20);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float4 f = src[i];
-                    x[4 * i] = f.x; x[4 * i + 1] = f.y; x[4 * i + 2] = f.z; x[4 * i + 3] = f.w;
+                __syncwarp();
+                if (q.in_pass) {
+                    const float4 x = *reinterpret_cast<const float4 *>(b + q.sub * d + 8 * q.u);
+                    const float4 y = *reinterpret_cast<const float4 *>(b + q.sub * d + 8 * q.u + 4);
+                    v.a[0] = make_float2(x.x, x.y);
+                    v.b[0] = make_float2(x.z, x.w);
+                    v.a[1] = make_float2(y.x, y.y);
+                    v.b[1] = make_float2(y.z, y.w);
                 }
             }
-            const float f = fac[chead & 63];
-            if (h.hadamard_b) hadamard_stages(x, h.hadamard_b, lane);
-            // the largest |x f| is |x|'s largest times f: rounding keeps the order
-            float amax = __fmul_rn(amax16(x), f);
-            const bool is_q = chd < h.q_heads;
-            const int64_t row = (is_q ? qrow : krow) + chd;
-            uint8_t *codes = (uint8_t *)(is_q ? h.q_out : h.k_out);
-            void *scales = is_q ? h.q_scales : h.k_scales;
+            if (h.hadamard_b) hadamard_heads<UNITS>(v, h.hadamard_b, lane);
+            float amax = fmaxf(fmaxf(fmaxf(fabsf(v.a[0].x), fabsf(v.a[0].y)), fmaxf(fabsf(v.a[1].x), fabsf(v.a[1].y))),
+                               fmaxf(fmaxf(fabsf(v.b[0].x), fabsf(v.b[0].y)), fmaxf(fabsf(v.b[1].x), fabsf(v.b[1].y))));
+            // the largest |v f| is the largest |v| times f: rounding keeps the order
+            amax = __fmul_rn(amax, f);
+            const int64_t row = (is_k ? krow : qrow) + now;
+            uint8_t *codes = (uint8_t *)(is_k ? h.k_out : h.q_out);
+            void *scales = is_k ? h.k_scales : h.q_scales;
+            float m = f, inv = 1.0f;   // a code is that of v m, or of (v f) inv
             if (F == kINT8Row) {
                 if (UNITS) {
-                    amax = group_max<(UNITS ? UNITS / 2 : 1)>(amax);
+                    amax = group_max<(UNITS ? UNITS : 1)>(amax);
                 } else {
 #pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) {   // maximum over the head's lanes
+                    for (int o = 16; o > 0; o >>= 1) {
                         const float y = __shfl_down_sync(0xFFFFFFFFu, amax, o);
-                        if (cc < o && cc + o < chunks) amax = fmaxf(amax, y);
+                        if (q.u < o && q.u + o < a.units) amax = fmaxf(amax, y);
                     }
-                    amax = __shfl_sync(0xFFFFFFFFu, amax, (lane - cc) & 31);
+                    amax = __shfl_sync(0xFFFFFFFFu, amax, lane - q.u);
                 }
                 const float s = pos < 0 ? __int_as_float(0x7FC00000) : __fdiv_rn(amax, 127.0f);
                 const Recip rs = recip_of(s);
                 if (valid) {
-                    float u[16];
-                    mul8(x, f, u);
-                    mul8(x + 8, f, u + 8);
-                    uint4 w = make_uint4(int_x4_quot(u, rs, 127), int_x4_quot(u + 4, rs, 127), int_x4_quot(u + 8, rs, 127),
-                                         int_x4_quot(u + 12, rs, 127));
-                    if (pos < 0) w = make_uint4(0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u);   // 1 x NaN
-                    *reinterpret_cast<uint4 *>(codes + (row * chunks + cc) * 16) = w;
-                    if (cc == 0) reinterpret_cast<float *>(scales)[row] = s;
+                    const float2 ff = make_float2(f, f);
+                    const float2 a0 = mul2(v.a[0], ff), a1 = mul2(v.a[1], ff), b0 = mul2(v.b[0], ff), b1 = mul2(v.b[1], ff);
+                    const float x[8] = {a0.x, b0.x, a0.y, b0.y, a1.x, b1.x, a1.y, b1.y};
+                    uint2 w = make_uint2(int_x4_quot(x, rs, 127), int_x4_quot(x + 4, rs, 127));
+                    if (pos < 0) w = make_uint2(0x01010101u, 0x01010101u);   // 1 x NaN
+                    *reinterpret_cast<uint2 *>(codes + row * d + 8 * q.u) = w;
+                    if (q.u == 0) reinterpret_cast<float *>(scales)[row] = s;
                 }
             } else {
-                amax = group_max<2>(amax);
+                amax = group_max<4>(amax);
                 const bool zero = !(amax > 0.0f);
-                float inv = 0.0f, z[16];
                 uint32_t sb = zero ? 127u : mx_scale(amax, F == kMXFP8 ? 8 : 2, inv);
                 if (pos < 0) sb = 255u;   // the NaN scale
-                // (x f) 2^-e rounded once, as x (f 2^-e) where that factor is finite and normal
-                const float m = __fmul_rn(f, inv);
-                if (m >= 1e-30f && m <= 1e30f) {
-                    mul8(x, m, z);
-                    mul8(x + 8, m, z + 8);
-                } else {
-                    mul8(x, f, z);
-                    mul8(x + 8, f, z + 8);
-                    mul8(z, inv, z);
-                    mul8(z + 8, inv, z + 8);
-                }
+                // (v f) 2^-e rounded once, as v (f 2^-e) where that factor is finite and normal
+                m = __fmul_rn(f, inv);
+                if (zero) m = 0.0f;
                 if (valid) {
-                    if (F == kMXFP8) {
-                        uint32_t w[4];
+                    if (!(m <= 1e30f) || (m < 1e-30f && !zero)) {
+                        m = inv;
+                        const float2 ff = make_float2(f, f);
 #pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            w[i] = zero ? 0u : cvt_e4m3x4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
-                        *reinterpret_cast<uint4 *>(codes + (row * chunks + cc) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                    } else {
-                        uint32_t w[2];
-#pragma unroll
-                        for (int i = 0; i < 2; i++)
-                            w[i] = zero ? 0u : cvt_e2m1x8(z[8 * i], z[8 * i + 1], z[8 * i + 2], z[8 * i + 3], z[8 * i + 4],
-                                                          z[8 * i + 5], z[8 * i + 6], z[8 * i + 7]);
-                        *reinterpret_cast<uint2 *>(codes + (row * chunks + cc) * 8) = make_uint2(w[0], w[1]);
+                        for (int i = 0; i < 2; i++) {
+                            v.a[i] = mul2(v.a[i], ff);
+                            v.b[i] = mul2(v.b[i], ff);
+                        }
                     }
-                    if (!(cc & 1)) reinterpret_cast<uint8_t *>(scales)[row * (chunks / 2) + cc / 2] = (uint8_t)sb;
+                    const float2 mm = make_float2(m, m);
+                    const float2 a0 = mul2(v.a[0], mm), a1 = mul2(v.a[1], mm), b0 = mul2(v.b[0], mm), b1 = mul2(v.b[1], mm);
+                    if (F == kMXFP8) {
+                        uint2 w = make_uint2(cvt_e4m3x4(a0.x, b0.x, a0.y, b0.y), cvt_e4m3x4(a1.x, b1.x, a1.y, b1.y));
+                        if (zero) w = make_uint2(0u, 0u);
+                        *reinterpret_cast<uint2 *>(codes + row * d + 8 * q.u) = w;
+                    } else {
+                        const uint32_t w = zero ? 0u : cvt_e2m1x8(a0.x, b0.x, a0.y, b0.y, a1.x, b1.x, a1.y, b1.y);
+                        *reinterpret_cast<uint32_t *>(codes + row * (d / 2) + 4 * q.u) = w;
+                    }
+                    if (!(q.u & 3)) reinterpret_cast<uint8_t *>(scales)[row * (d / 32) + q.u / 4] = (uint8_t)sb;
                 }
             }
         }
@@ -495,16 +517,13 @@ cudaError_t launch_qk_norm_rope(const HeadArgs &h, cudaStream_t s) {
     a.units = h.head_dim / 8;
     a.per_pass = 32 / a.units;
     a.passes = (h.q_heads + h.k_heads + a.per_pass - 1) / a.per_pass;
-    // Few tokens: spread a token's heads over warps, in steps of the two
-    // passes that the quantizing kernel takes together, down to one step a
-    // warp; many: a warp does up to 16 passes and reads its angles once.
+    // Few tokens: a token's heads are spread over warps, down to one pass each;
+    // many: a warp does up to 16 passes and reads its angles once.
     const int64_t want = (int64_t)sm_count() * 16;   // warps that fill the device
     int64_t per = h.tokens * a.passes / want;
-    per = per < 2 ? 2 : per > 16 ? 16 : per / 2 * 2;
-    if (h.fmt < 0 && h.tokens * a.passes < want) per = 1;
+    per = per < 1 ? 1 : per > 16 ? 16 : per;
     a.items = (int)((a.passes + per - 1) / per);
-    per = (a.passes + a.items - 1) / a.items;   // a token's warps take equal shares
-    a.per_item = (int)(per == 1 ? 1 : (per + 1) / 2 * 2);
+    a.per_item = (a.passes + a.items - 1) / a.items;   // a token's warps take equal shares
     a.items = (a.passes + a.per_item - 1) / a.per_item;
     const cudaError_t e = error_word_address(&a.err);
     if (e != cudaSuccess) return e;
