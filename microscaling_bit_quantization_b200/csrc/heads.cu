@@ -12,11 +12,15 @@
 // both ends of its pairs: 8 consecutive ones when pairs are neighbours
 // (interleaved) or lie behind `rot`, else 4 of the first and the 4 partners of
 // the second half.  A head takes U = D / 8 neighbouring lanes, a warp
-// floor(32 / U) heads at a time, all of one token, so a lane's four angles
-// are loaded once and serve every head it meets (they would otherwise be
-// read twice as often as the data).  Sums run over the U lanes by a shuffle
-// tree.  Bound: HBM; the next heads' loads are in flight while the present
-// ones are normed.
+// floor(32 / U) heads at a time (a pass).  A warp's work is an item: up to 8
+// passes over the q heads, or the k heads, of one token, so that a lane's
+// weights and angles, joined to one linear map, serve them all and pointers
+// only step.  Sums run over the U lanes by shuffles: butterflies where U is a
+// power of two, else a tree.
+// Bound: instruction issue and latency together (8192 tokens x 40 heads x 128
+// in bf16: 41 us, 4.2 TB/s, 137 instructions per pass of 256 elements, 56% of
+// issue slots used; items of 16 passes 48 us, of 4 40 us, of 2 52 us: a long
+// item leaves warps idle at the end, a short one reads its angles again).
 #include <cuda_runtime.h>
 
 #include "groups.cuh"
@@ -29,13 +33,16 @@ namespace {
 
 constexpr int kHeadThreads = 128;
 constexpr int kHeadWarps = kHeadThreads / 32;
+constexpr int kHeadPasses = 8;   // of an item, at most
 
 struct HeadKernelArgs {
     HeadArgs h;
-    int units;              // lanes per head
-    int per_pass;           // heads a warp takes at a time
-    int passes, per_item;   // passes over a token's heads, and how many of them one warp does
-    int items;              // warps per token
+    int units;          // lanes per head
+    int per_pass;       // heads a warp takes at a time
+    int per_item;       // such passes that make an item, a warp's work; an item lies on one side, q or k
+    int q_items;        // of a token, then those of its k heads
+    FastDiv items;      // of a token
+    uint32_t total;     // of all tokens
     unsigned int *err;
 };
 
@@ -68,18 +75,18 @@ struct Raw {
     uint4 w[sizeof(T) / 2];
 };
 template <bool IL>
-__device__ __forceinline__ void load_raw(Raw<__nv_bfloat16> &r, const __nv_bfloat16 *x, int p0, int p1) {
+__device__ __forceinline__ void load_raw(Raw<__nv_bfloat16> &r, const __nv_bfloat16 *x, int apart) {   // x: the first group
     if (IL) {
-        r.w[0] = *reinterpret_cast<const uint4 *>(x + p0);
+        r.w[0] = *reinterpret_cast<const uint4 *>(x);
     } else {
-        const uint2 a = *reinterpret_cast<const uint2 *>(x + p0), b = *reinterpret_cast<const uint2 *>(x + p1);
+        const uint2 a = *reinterpret_cast<const uint2 *>(x), b = *reinterpret_cast<const uint2 *>(x + apart);
         r.w[0] = make_uint4(a.x, a.y, b.x, b.y);
     }
 }
 template <bool IL>
-__device__ __forceinline__ void load_raw(Raw<float> &r, const float *x, int p0, int p1) {
-    r.w[0] = *reinterpret_cast<const uint4 *>(x + p0);
-    r.w[1] = *reinterpret_cast<const uint4 *>(x + p1);
+__device__ __forceinline__ void load_raw(Raw<float> &r, const float *x, int apart) {
+    r.w[0] = *reinterpret_cast<const uint4 *>(x);
+    r.w[1] = *reinterpret_cast<const uint4 *>(x + apart);
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -130,30 +137,30 @@ __device__ __forceinline__ void in_order(const Pairs &v, float4 &x, float4 &y) {
     }
 }
 template <bool IL>
-__device__ __forceinline__ void store_raw(__nv_bfloat16 *o, int p0, int p1, const Pairs &v) {
+__device__ __forceinline__ void store_raw(__nv_bfloat16 *o, int apart, const Pairs &v) {
     float4 x, y;
     in_order<IL>(v, x, y);
     const uint2 a = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
     const uint2 b = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
     if (IL) {
-        *reinterpret_cast<uint4 *>(o + p0) = make_uint4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<uint4 *>(o) = make_uint4(a.x, a.y, b.x, b.y);
     } else {
-        *reinterpret_cast<uint2 *>(o + p0) = a;
-        *reinterpret_cast<uint2 *>(o + p1) = b;
+        *reinterpret_cast<uint2 *>(o) = a;
+        *reinterpret_cast<uint2 *>(o + apart) = b;
     }
 }
 template <bool IL>
-__device__ __forceinline__ void store_raw(float *o, int p0, int p1, const Pairs &v) {
+__device__ __forceinline__ void store_raw(float *o, int apart, const Pairs &v) {
     float4 x, y;
     in_order<IL>(v, x, y);
-    *reinterpret_cast<float4 *>(o + p0) = x;
-    *reinterpret_cast<float4 *>(o + p1) = y;
+    *reinterpret_cast<float4 *>(o) = x;
+    *reinterpret_cast<float4 *>(o + apart) = y;
 }
 
 // Weight and rotation of a lane's pairs as one linear map:
 // a' = aa a + ab b, b' = bb b + ba a with aa = w_a c, ab = -w_b s, bb = w_b c,
-// ba = w_a s; for elements behind rot_dim a' = w_a a, b' = w_b b.  It changes
-// with the token and from q to k only.
+// ba = w_a s; for elements behind rot_dim a' = w_a a, b' = w_b b.  One serves
+// an item.
 struct Turn {
     float2 aa[2], ab[2], bb[2], ba[2];
 };
@@ -248,58 +255,85 @@ struct LanePlace {
         u = lane % units;
         sub = lane / units;
         in_pass = UNITS ? true : sub < a.per_pass;
-        if (!in_pass) u = 32;   // takes no part in a sum
         turned = in_pass && 8 * u < a.h.rot;
         p0 = turned && !IL ? 4 * u : 8 * u;
         p1 = turned && !IL ? a.h.rot / 2 + 4 * u : 8 * u + 4;
+        if (!in_pass) {   // a lane past the last head: no part in a sum, and its weights are read from the first ones
+            u = 32;
+            p0 = 0;
+            p1 = 4;
+        }
+    }
+};
+
+// An item: a run of neighbouring heads of one token, all q or all k.
+template <typename T>
+struct HeadItem {
+    bool is_k;
+    int64_t t, pos;
+    int head, end, passes;   // this lane's first head, the side's number of heads, passes of the item
+    const T *x;              // this lane's elements of that head
+    __device__ __forceinline__ HeadItem(const HeadKernelArgs &a, uint32_t item, int sub, bool in_pass, int p0) {
+        const uint32_t token = fdiv(item, a.items), i = item - token * a.items.d;
+        is_k = (int)i >= a.q_items;
+        t = token;
+        end = is_k ? a.h.k_heads : a.h.q_heads;
+        const int first = (int)(is_k ? i - a.q_items : i) * a.per_item * a.per_pass;
+        const int left = (end - first + a.per_pass - 1) / a.per_pass;
+        passes = left < a.per_item ? left : a.per_item;
+        head = first + sub;
+        if (!in_pass) end = 0;   // lanes past the last head have none
+        x = (is_k ? (const T *)a.h.k + t * a.h.k_stride : (const T *)a.h.q + t * a.h.q_stride) + (int64_t)head * a.h.head_dim + p0;
     }
 };
 
 template <typename T, int UNITS, bool IL>
-__global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope(HeadKernelArgs a) {
+__global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope(HeadKernelArgs a) {
+    constexpr int kDepth = 4;   // passes whose loads are in flight
     const HeadArgs &h = a.h;
     const int lane = threadIdx.x & 31;
     const LanePlace<UNITS, IL> q(a, lane);
-    const int heads = h.q_heads + h.k_heads, d = h.head_dim;
+    const int step = a.per_pass * h.head_dim, apart = q.p1 - q.p0;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t total = h.tokens * a.items;
-    for (int64_t it = (int64_t)blockIdx.x * kHeadWarps + (threadIdx.x >> 5); it < total;
-         it += (int64_t)gridDim.x * kHeadWarps) {
-        const int64_t t = a.items == 1 ? it : it / a.items;
-        const int pass0 = (int)(it - t * a.items) * a.per_item;
-        const int pass1 = pass0 + a.per_item < a.passes ? pass0 + a.per_item : a.passes;
-        // head i of the token at qx + i d, or kx + i d for the k heads
-        const T *qx = (const T *)h.q + t * h.q_stride, *kx = (const T *)h.k + t * h.k_stride - (int64_t)h.q_heads * d;
-        T *qy = (T *)h.q_out + t * h.q_out_stride, *ky = (T *)h.k_out + t * h.k_out_stride - (int64_t)h.q_heads * d;
-        const int end = pass1 * a.per_pass < heads ? pass1 * a.per_pass : heads;
-        int head = q.in_pass ? pass0 * a.per_pass + q.sub : end;
-        Raw<T> next = {};
-        if (head < end) load_raw<IL>(next, (head < h.q_heads ? qx : kx) + (int64_t)head * d, q.p0, q.p1);
-        const int64_t pos = position_of(h, t, a.err);
-        Turn turn = {};
-        int side = -1;   // whose weight `turn` holds
-        for (int pass = pass0; pass < pass1; pass++) {
-            Pairs v = unpack<IL>(next);
-            const int now = head;
-            head += a.per_pass;
-            if (head < end) load_raw<IL>(next, (head < h.q_heads ? qx : kx) + (int64_t)head * d, q.p0, q.p1);
-            const int is_k = now >= h.q_heads;
-            if (is_k != side && now < end) {
-                side = is_k;
-                turn = turn_of<IL>(h, is_k ? h.k_weight : h.q_weight, q.u, q.p0, q.p1, q.turned, pos < 0 ? 0 : pos);
-            }
-            float r = norm_turn<UNITS>(v, h, turn, q.turned, q.u, a.units, lane);
-            if (pos < 0) r = __int_as_float(0x7FC00000);
-            if (now < end) {
-                // a lane stores the elements it loaded and no others: q_out = q and k_out = k are allowed
-                const float2 rr = make_float2(r, r);
+    for (uint32_t item = blockIdx.x * kHeadWarps + (threadIdx.x >> 5); item < a.total; item += gridDim.x * kHeadWarps) {
+        HeadItem<T> in(a, item, q.sub, q.in_pass, q.p0);
+        Raw<T> raw[kDepth] = {};
+        int ahead = in.head;
+        auto fetch = [&](Raw<T> &r) {
+            if (ahead < in.end) load_raw<IL>(r, in.x, apart);
+            ahead += a.per_pass;
+            in.x += step;
+        };
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    v.a[i] = mul2(v.a[i], rr);
-                    v.b[i] = mul2(v.b[i], rr);
+        for (int j = 0; j < kDepth; j++)
+            if (j < in.passes) fetch(raw[j]);
+        const int64_t pos = position_of(h, in.t, a.err);
+        const Turn turn = turn_of<IL>(h, in.is_k ? h.k_weight : h.q_weight, q.u, q.p0, q.p1, q.turned, pos < 0 ? 0 : pos);
+        T *y = (in.is_k ? (T *)h.k_out + in.t * h.k_out_stride : (T *)h.q_out + in.t * h.q_out_stride) +
+               (int64_t)in.head * h.head_dim + q.p0;
+#pragma unroll 1
+        for (int pass = 0; pass < in.passes; pass += kDepth) {
+#pragma unroll
+            for (int j = 0; j < kDepth; j++) {
+                if (pass + j < in.passes) {
+                    Pairs v = unpack<IL>(raw[j]);
+                    if (pass + j + kDepth < in.passes) fetch(raw[j]);
+                    float r = norm_turn<UNITS>(v, h, turn, q.turned, q.u, a.units, lane);
+                    if (pos < 0) r = __int_as_float(0x7FC00000);
+                    if (in.head < in.end) {
+                        // a lane stores the elements it loaded and no others: q_out = q and k_out = k are allowed
+                        const float2 rr = make_float2(r, r);
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            v.a[i] = mul2(v.a[i], rr);
+                            v.b[i] = mul2(v.b[i], rr);
+                        }
+                        store_raw<IL>(y, apart, v);
+                    }
+                    in.head += a.per_pass;
+                    y += step;
                 }
-                store_raw<IL>((is_k ? ky : qy) + (int64_t)now * d, q.p0, q.p1, v);
             }
         }
     }
@@ -352,44 +386,37 @@ __device__ __forceinline__ void hadamard_heads(Pairs &v, int b, int lane) {
 // them so; pairs of halves go through shared memory (1 KB per warp), stored so
 // that both 16-byte reads give even and odd elements apart.  The head's factor
 // and 1/sqrt(b) are applied where the codes are formed.  Bound: instruction
-// issue, most of it the rotation's 8 exchanges per stage.
+// issue (the same heads to MXFP8: 44 us, with a Hadamard rotation of 128 58 us,
+// half of what it adds being the four exchanges of 8 values across lanes).
 template <typename T, int F, int UNITS, bool IL>
-__global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope_quantize(HeadKernelArgs a) {
+__global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope_quantize(HeadKernelArgs a) {
     __shared__ __align__(16) float buf[IL ? 1 : kHeadWarps][IL ? 4 : 256];
     const HeadArgs &h = a.h;
     const int lane = threadIdx.x & 31;
     float *b = buf[IL ? 0 : threadIdx.x >> 5];
     const LanePlace<UNITS, IL> q(a, lane);
-    const int heads = h.q_heads + h.k_heads, d = h.head_dim;
+    const int d = h.head_dim, step = a.per_pass * d, apart = q.p1 - q.p0;
     const float norm = h.hadamard_b ? __frsqrt_rn((float)h.hadamard_b) : 1.0f;
+    constexpr int kPerByte = F == kMXFP4 ? 2 : 1;
+    const int code_step = step / kPerByte, scale_step = a.per_pass * (F == kINT8Row ? 4 : d / 32);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t total = h.tokens * a.items;
-    for (int64_t it = (int64_t)blockIdx.x * kHeadWarps + (threadIdx.x >> 5); it < total;
-         it += (int64_t)gridDim.x * kHeadWarps) {
-        const int64_t t = a.items == 1 ? it : it / a.items;
-        const int pass0 = (int)(it - t * a.items) * a.per_item;
-        const int pass1 = pass0 + a.per_item < a.passes ? pass0 + a.per_item : a.passes;
-        const T *qx = (const T *)h.q + t * h.q_stride, *kx = (const T *)h.k + t * h.k_stride - (int64_t)h.q_heads * d;
-        const int end = pass1 * a.per_pass < heads ? pass1 * a.per_pass : heads;
-        const int64_t qrow = t * h.q_heads, krow = t * h.k_heads - h.q_heads;   // row of head i: qrow + i or krow + i
-        int head = q.in_pass ? pass0 * a.per_pass + q.sub : end;
-        Raw<T> next = {};
-        if (head < end) load_raw<IL>(next, (head < h.q_heads ? qx : kx) + (int64_t)head * d, q.p0, q.p1);
-        const int64_t pos = position_of(h, t, a.err);
-        Turn turn = {};
-        int side = -1;
-        for (int pass = pass0; pass < pass1; pass++) {
-            Pairs v = unpack<IL>(next);
-            const int now = head;
-            const bool valid = now < end;
-            head += a.per_pass;
-            if (head < end) load_raw<IL>(next, (head < h.q_heads ? qx : kx) + (int64_t)head * d, q.p0, q.p1);
-            const int is_k = now >= h.q_heads;
-            if (is_k != side && valid) {
-                side = is_k;
-                turn = turn_of<IL>(h, is_k ? h.k_weight : h.q_weight, q.u, q.p0, q.p1, q.turned, pos < 0 ? 0 : pos);
-            }
+    for (uint32_t item = blockIdx.x * kHeadWarps + (threadIdx.x >> 5); item < a.total; item += gridDim.x * kHeadWarps) {
+        HeadItem<T> in(a, item, q.sub, q.in_pass, q.p0);
+        Raw<T> raw = {};
+        if (in.head < in.end) load_raw<IL>(raw, in.x, apart);
+        const int64_t pos = position_of(h, in.t, a.err);
+        const Turn turn = turn_of<IL>(h, in.is_k ? h.k_weight : h.q_weight, q.u, q.p0, q.p1, q.turned, pos < 0 ? 0 : pos);
+        const int64_t row = in.t * (in.is_k ? h.k_heads : h.q_heads) + in.head;
+        uint8_t *codes = (uint8_t *)(in.is_k ? h.k_out : h.q_out) + (row * d + 8 * q.u) / kPerByte;
+        uint8_t *scales = (uint8_t *)(in.is_k ? h.k_scales : h.q_scales) + (F == kINT8Row ? row * 4 : row * (d / 32) + q.u / 4);
+#pragma unroll 1
+        for (int pass = 0; pass < in.passes; pass++) {
+            Pairs v = unpack<IL>(raw);
+            const bool valid = in.head < in.end;
+            in.head += a.per_pass;
+            in.x += step;
+            if (in.head < in.end && pass + 1 < in.passes) load_raw<IL>(raw, in.x, apart);
             const float f = norm_turn<UNITS>(v, h, turn, q.turned, q.u, a.units, lane) * norm;
             if (!IL) {
                 __syncwarp();   // the pass before has been read
@@ -412,10 +439,6 @@ __global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope_quantize(HeadKern
                                fmaxf(fmaxf(fabsf(v.b[0].x), fabsf(v.b[0].y)), fmaxf(fabsf(v.b[1].x), fabsf(v.b[1].y))));
             // the largest |v f| is the largest |v| times f: rounding keeps the order
             amax = __fmul_rn(amax, f);
-            const int64_t row = (is_k ? krow : qrow) + now;
-            uint8_t *codes = (uint8_t *)(is_k ? h.k_out : h.q_out);
-            void *scales = is_k ? h.k_scales : h.q_scales;
-            float m = f, inv = 1.0f;   // a code is that of v m, or of (v f) inv
             if (F == kINT8Row) {
                 if (UNITS) {
                     amax = group_max<(UNITS ? UNITS : 1)>(amax);
@@ -435,19 +458,19 @@ __global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope_quantize(HeadKern
                     const float x[8] = {a0.x, b0.x, a0.y, b0.y, a1.x, b1.x, a1.y, b1.y};
                     uint2 w = make_uint2(int_x4_quot(x, rs, 127), int_x4_quot(x + 4, rs, 127));
                     if (pos < 0) w = make_uint2(0x01010101u, 0x01010101u);   // 1 x NaN
-                    *reinterpret_cast<uint2 *>(codes + row * d + 8 * q.u) = w;
-                    if (q.u == 0) reinterpret_cast<float *>(scales)[row] = s;
+                    *reinterpret_cast<uint2 *>(codes) = w;
+                    if (q.u == 0) *reinterpret_cast<float *>(scales) = s;
                 }
             } else {
                 amax = group_max<4>(amax);
                 const bool zero = !(amax > 0.0f);
+                float inv = 0.0f;
                 uint32_t sb = zero ? 127u : mx_scale(amax, F == kMXFP8 ? 8 : 2, inv);
                 if (pos < 0) sb = 255u;   // the NaN scale
                 // (v f) 2^-e rounded once, as v (f 2^-e) where that factor is finite and normal
-                m = __fmul_rn(f, inv);
-                if (zero) m = 0.0f;
+                float m = __fmul_rn(f, inv);
                 if (valid) {
-                    if (!(m <= 1e30f) || (m < 1e-30f && !zero)) {
+                    if (!(m >= 1e-30f && m <= 1e30f) && !zero) {
                         m = inv;
                         const float2 ff = make_float2(f, f);
 #pragma unroll
@@ -461,21 +484,22 @@ __global__ void __launch_bounds__(kHeadThreads) k_qk_norm_rope_quantize(HeadKern
                     if (F == kMXFP8) {
                         uint2 w = make_uint2(cvt_e4m3x4(a0.x, b0.x, a0.y, b0.y), cvt_e4m3x4(a1.x, b1.x, a1.y, b1.y));
                         if (zero) w = make_uint2(0u, 0u);
-                        *reinterpret_cast<uint2 *>(codes + row * d + 8 * q.u) = w;
+                        *reinterpret_cast<uint2 *>(codes) = w;
                     } else {
                         const uint32_t w = zero ? 0u : cvt_e2m1x8(a0.x, b0.x, a0.y, b0.y, a1.x, b1.x, a1.y, b1.y);
-                        *reinterpret_cast<uint32_t *>(codes + row * (d / 2) + 4 * q.u) = w;
+                        *reinterpret_cast<uint32_t *>(codes) = w;
                     }
-                    if (!(q.u & 3)) reinterpret_cast<uint8_t *>(scales)[row * (d / 32) + q.u / 4] = (uint8_t)sb;
+                    if (!(q.u & 3)) *scales = (uint8_t)sb;
                 }
             }
+            codes += code_step;
+            scales += scale_step;
         }
     }
 }
 
 cudaError_t launch_heads(void (*k)(HeadKernelArgs), const HeadKernelArgs &a, cudaStream_t s) {
-    const int64_t warps = a.h.tokens * a.items;
-    int64_t ctas = (warps + kHeadWarps - 1) / kHeadWarps;
+    int64_t ctas = ((int64_t)a.total + kHeadWarps - 1) / kHeadWarps;
     const int64_t cap = (int64_t)sm_count() * 64;
     if (ctas > cap) ctas = cap;
     cudaLaunchConfig_t cfg = {};
@@ -516,15 +540,17 @@ cudaError_t launch_qk_norm_rope(const HeadArgs &h, cudaStream_t s) {
     a.h = h;
     a.units = h.head_dim / 8;
     a.per_pass = 32 / a.units;
-    a.passes = (h.q_heads + h.k_heads + a.per_pass - 1) / a.per_pass;
     // Few tokens: a token's heads are spread over warps, down to one pass each;
     // many: a warp does up to 16 passes and reads its angles once.
-    const int64_t want = (int64_t)sm_count() * 16;   // warps that fill the device
-    int64_t per = h.tokens * a.passes / want;
-    per = per < 1 ? 1 : per > 16 ? 16 : per;
-    a.items = (int)((a.passes + per - 1) / per);
-    a.per_item = (a.passes + a.items - 1) / a.items;   // a token's warps take equal shares
-    a.items = (a.passes + a.per_item - 1) / a.per_item;
+    const int64_t qp = (h.q_heads + a.per_pass - 1) / a.per_pass, kp = (h.k_heads + a.per_pass - 1) / a.per_pass;
+    int64_t per = h.tokens * (qp + kp) / ((int64_t)sm_count() * 16);
+    per = per < 1 ? 1 : per > kHeadPasses ? kHeadPasses : per;
+    while (h.tokens * ((qp + per - 1) / per + (kp + per - 1) / per) >= ((int64_t)1 << 31)) per *= 2;   // items are counted in 31 bits
+    a.per_item = (int)per;
+    a.q_items = (int)((qp + per - 1) / per);
+    const int64_t items = a.q_items + (kp + per - 1) / per;
+    a.items = make_fastdiv((uint32_t)items);
+    a.total = (uint32_t)(h.tokens * items);
     const cudaError_t e = error_word_address(&a.err);
     if (e != cudaSuccess) return e;
     if (h.bf16) return h.interleaved ? pick_units<__nv_bfloat16, true>(a, s) : pick_units<__nv_bfloat16, false>(a, s);
