@@ -43,7 +43,6 @@
 
 #include <cstring>
 
-#include "groups.cuh"
 #include "mxq_formats.cuh"
 #include "mxq_internal.h"
 #include "tc_ptx.cuh"
@@ -107,78 +106,9 @@ struct GemmParams {
     void *y;
     int m, n, kbytes, num_k_tiles, s4, has_lowrank, y_bf16, y_tma;
     int m_tiles, n_tiles;         // 256 x 256 tiles
+    int sfa_tiles;                // 128-row scale tiles of A (rows padded to 128)
     unsigned long long wait_ns;
-    // grouped launches: rows of A and Y in expert order, group g's B the g-th of B's n rows
-    const int32_t *offsets;
-    int n_groups;
 };
-
-// One output tile: 256 rows from pm0 (those below row_end stored), 256 columns
-// from n0 of group `group`'s B; sf0: the 128-row scale tile of row pm0.
-struct Tile {
-    int pm0, row_end, n0, sf0, group;
-};
-// Grouped launches: the 128-row scale tiles (low half) and the 256-row output
-// tiles (high half) before each group.
-constexpr int kTableBytes = 4 * (kMaxGroups + 1);
-__device__ __forceinline__ Tile tile_at(const GemmParams &p, int tile) {
-    Tile t;
-    t.pm0 = (tile / p.n_tiles) * 256;
-    t.row_end = p.m;
-    t.n0 = (tile % p.n_tiles) * BN;
-    t.sf0 = t.pm0 >> 7;
-    t.group = 0;
-    return t;
-}
-__device__ __forceinline__ Tile tile_in_groups(const GemmParams &p, const uint32_t *table, int tile) {
-    const int mt = tile / p.n_tiles;
-    int lo = 0, hi = p.n_groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((int)(table[mid] >> 16) <= mt) lo = mid;
-        else hi = mid;
-    }
-    const int within = mt - (int)(table[lo] >> 16);
-    Tile t;
-    t.group = lo;
-    t.pm0 = clamp_row(__ldg(p.offsets + lo), p.m) + within * 256;
-    t.row_end = clamp_row(__ldg(p.offsets + lo + 1), p.m);
-    t.n0 = (tile % p.n_tiles) * BN;
-    t.sf0 = (int)(table[lo] & 0xFFFFu) + within * 2;
-    return t;
-}
-// Fills the table (warp 0) and reports offsets that had to be clamped.
-__device__ __forceinline__ void fill_table(const GemmParams &p, uint32_t *table, unsigned int *err) {
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        uint32_t sf = 0, mt = 0;   // tiles before this step's groups
-        for (int b = 0; b < p.n_groups; b += 32) {
-            const int g = b + lane;
-            uint32_t c = 0, w = 0;
-            if (g < p.n_groups) {
-                const int o0 = p.offsets[g], o1 = p.offsets[g + 1];
-                const int r = clamp_row(o1, p.m) - clamp_row(o0, p.m);
-                if (o0 < 0 || o1 < o0 || o1 > p.m) latch_index_error(err);
-                c = r > 0 ? (uint32_t)(r + 127) >> 7 : 0u;
-                w = r > 0 ? (uint32_t)(r + 255) >> 8 : 0u;
-            }
-            uint32_t ci = c, wi = w;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, ci, o), y = __shfl_up_sync(0xFFFFFFFFu, wi, o);
-                if (lane >= o) {
-                    ci += x;
-                    wi += y;
-                }
-            }
-            // offsets in order stay below 2^16 (kMaxGroupedRows); others are held there
-            if (g < p.n_groups) table[g] = min(sf + ci - c, 0xFFFFu) | (min(mt + wi - w, 0xFFFFu) << 16);
-            sf += __shfl_sync(0xFFFFFFFFu, ci, 31);
-            mt += __shfl_sync(0xFFFFFFFFu, wi, 31);
-        }
-        if (lane == 0) table[p.n_groups] = min(sf, 0xFFFFu) | (min(mt, 0xFFFFu) << 16);
-    }
-}
 
 // ------------------------------------------------------------------ PTX
 
@@ -326,7 +256,7 @@ __device__ __forceinline__ void mma_kstep(uint32_t acc_addr, uint64_t ad, uint64
     }
 }
 
-template <int KIND, bool GROUPED>
+template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_gemm(const __grid_constant__ GemmParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -346,10 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const uint32_t rank = cluster_rank();
     const int cid = (int)cluster_id(), ncl = (int)cluster_count();
     constexpr int NSF = sf_atoms<KIND>();
-    uint32_t *table = reinterpret_cast<uint32_t *>(epi + EPI_BYTES + BAR_BYTES);   // grouped launches
-    int num_tiles = p.m_tiles * p.n_tiles;
-    const int sfb_tiles = (p.n + 127) >> 7;   // of a group's B
-    auto at = [&](int tile) { return GROUPED ? tile_in_groups(p, table, tile) : tile_at(p, tile); };
+    const int num_tiles = p.m_tiles * p.n_tiles;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; s++) {
@@ -380,25 +307,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     // are read and Y written only after it has completed
     pdl_wait();
     pdl_launch_dependents();
-    if (GROUPED) {
-        fill_table(p, table, blockIdx.x == 0 ? &g_error_word : nullptr);
-        __syncthreads();
-        const int mt = (int)(table[p.n_groups] >> 16);   // above m_tiles only for offsets out of order
-        num_tiles = (mt < p.m_tiles ? mt : p.m_tiles) * p.n_tiles;
-    }
 
     if (warp == 0) {
         // ---------------------------------------------------------- producer (both CTAs)
         if (lane == 0) {
             int it = 0, issued = 0;
             for (int tile = cid; tile < num_tiles && !*abort_flag; tile += ncl) {
-                const Tile t = at(tile);
-                const int m0 = t.pm0 + (int)rank * BM, nb0 = t.group * p.n + t.n0 + (int)rank * BNH;
-                const int rt_a = t.sf0 + (int)rank;
-                const bool sfa_mine = m0 < t.row_end;
-                const bool sfa_peer = t.pm0 + BM < t.row_end;
-                const bool b_hi = (t.n0 + 128) < p.n;
-                const int rt_b = t.group * sfb_tiles + (t.n0 >> 7);
+                const int pm0 = (tile / p.n_tiles) * 256, n0 = (tile % p.n_tiles) * BN;
+                const int m0 = pm0 + (int)rank * BM, nb0 = n0 + (int)rank * BNH;
+                const int rt_a = (pm0 >> 7) + (int)rank;
+                const bool sfa_mine = rt_a < p.sfa_tiles;
+                const bool sfa_peer = (pm0 >> 7) + 1 < p.sfa_tiles;
+                const bool b_hi = (n0 + 128) < p.n;
+                const int rt_b = n0 >> 7;
                 for (int kt = 0; kt < nsteps; kt++, it++) {
                     const int s = it % STAGES;
                     const uint32_t ph = (it / STAGES) & 1;
@@ -558,20 +479,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const uint32_t acce_leader0 = map_to_rank(acce, 0), acce_leader1 = map_to_rank(acce + 1, 0);
         uint8_t *stage_buf = epi + q * 2 * EPI_BUF;
         const bool vec = p.y_bf16 ? (p.n % 8 == 0) : (p.n % 4 == 0);
-        // the tensor scales hold for the whole launch (grouped: for a group): read once, outside the tile loop
+        // the tensor scales hold for the whole launch: read once, outside the tile loop
         float alpha = 1.0f;
-        if (!GROUPED && (KIND == kKindNVFP4 || KIND == kKindFP8)) alpha = __fmul_rn(__ldg(p.a_ts), __ldg(p.b_ts));
+        if (KIND == kKindNVFP4 || KIND == kKindFP8) alpha = __fmul_rn(__ldg(p.a_ts), __ldg(p.b_ts));
         if (KIND == kKindBF16 && p.b_ts) alpha = __ldg(p.b_ts);
         int tcount = 0, sub = 0;
         for (int tile = cid; tile < num_tiles; tile += ncl, tcount++) {
-            const Tile t = at(tile);
-            const int n0 = t.n0;
-            const int row0 = t.pm0 + (int)rank * BM + q * 32;
+            const int pm0 = (tile / p.n_tiles) * 256, n0 = (tile % p.n_tiles) * BN;
+            const int row0 = pm0 + (int)rank * BM + q * 32;
             const int row = row0 + lane;
-            // a TMA store writes 32 whole rows: where a group ends among them, the rows are stored singly
-            const bool tma_rows = p.y_tma && (!GROUPED || row0 + 32 <= t.row_end);
-            if (GROUPED && (KIND == kKindNVFP4 || KIND == kKindFP8)) alpha = __fmul_rn(__ldg(p.a_ts), __ldg(p.b_ts + t.group));
-            const float *sbn = p.b_row_scale + (GROUPED ? (int64_t)t.group * p.n : 0);
             const int st = tcount & 1;
             bool ok = !*abort_flag && mbar_wait(accf + st, (tcount >> 1) & 1, p.wait_ns);
             ok = __all_sync(0xFFFFFFFFu, ok);
@@ -585,15 +501,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             constexpr int OVL = ovl_chunks<KIND>();
             static_assert(KIND != kKindINT8 || OVL == 0, "the INT8 row scale is read before any chunk");
             float ra = 0.0f;   // INT8 row scale
-            const bool row_ok = row < t.row_end;
+            const bool row_ok = row < p.m;
             // The shared columns (the last OVL_CHUNKS chunks of stage 0, the first OVL_CHUNKS of
             // stage 1) go to registers first and are released at once, so the next tile's MMAs
             // wait only for these loads; then every chunk is scaled, staged and stored.
             auto process = [&](const int c, const uint32_t (&r)[32]) {
                     const int nb = n0 + c * 32;
                     float v[32];
-                    scale_chunk<KIND>(r, v, alpha, ra, sbn + nb, p.n - nb);
-                    if (tma_rows) {
+                    scale_chunk<KIND>(r, v, alpha, ra, p.b_row_scale + nb, p.n - nb);
+                    if (p.y_tma) {
                         // swizzled staging of this 32-column chunk, then one TMA store of 32 rows:
                         // bf16 rows of 64 B (64B swizzle: 16-byte unit j of row t at t*64 + (j ^ ((t >> 1) & 3))*16),
                         // fp32 rows of 128 B (128B swizzle: unit j at t*128 + (j ^ (t & 7))*16)
@@ -723,24 +639,21 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint6
 
 namespace {
 
-template <int KIND, bool GROUPED = false>
+template <int KIND>
 cudaError_t launch_kind(const GemmParams &p, int grid, cudaStream_t s) {
-    constexpr int smem_bytes = SMEM_BYTES + (GROUPED ? kTableBytes : 0);
-    static_assert(smem_bytes <= 227 * 1024, "shared memory budget");
     static PerDeviceOnce smem_opt_in;
-    cudaError_t e = smem_opt_in.run([] {
-        return cudaFuncSetAttribute(k_gemm<KIND, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
-    });
+    cudaError_t e = smem_opt_in.run(
+        [] { return cudaFuncSetAttribute(k_gemm<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES); });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid, 1, 1);   // clusters of 2 from __cluster_dims__
     cfg.blockDim = dim3(kGemmThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem_bytes;
+    cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = s;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_gemm<KIND, GROUPED>, p);
+    return cudaLaunchKernelEx(&cfg, k_gemm<KIND>, p);
 }
 
 }  // namespace
@@ -791,6 +704,7 @@ static cudaError_t launch_gemm_common(const GemmOperands &op, bool bf16_operands
     p.y_bf16 = op.y_bf16;
     p.m_tiles = (int)((op.m + 255) / 256);
     p.n_tiles = (int)((op.n + BN - 1) / BN);
+    p.sfa_tiles = (int)((op.m + 127) / 128);
     p.wait_ns = 2000000000ull;   // 2 s
     const int sms = sm_count();
     const int tiles = p.m_tiles * p.n_tiles;
@@ -810,59 +724,6 @@ static cudaError_t launch_gemm_common(const GemmOperands &op, bool bf16_operands
 cudaError_t launch_qlinear(const GemmOperands &op, cudaStream_t s) { return launch_gemm_common(op, false, s); }
 
 cudaError_t launch_gemm_bf16(const GemmOperands &op, cudaStream_t s) { return launch_gemm_common(op, true, s); }
-
-// Rows in expert order: the same kernel over a list of tiles that each CTA
-// pair derives from the device offsets, each tile within one group.
-cudaError_t launch_qlinear_grouped_many(const GroupedOperands &op, cudaStream_t s) {
-    GemmParams p;
-    memset(&p, 0, sizeof(p));
-    const int64_t kbytes = fmt_is4(op.fmt) ? op.k / 2 : op.k;
-    const auto SW128 = CU_TENSOR_MAP_SWIZZLE_128B, NOSW = CU_TENSOR_MAP_SWIZZLE_NONE;
-    const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, U64 = CU_TENSOR_MAP_DATA_TYPE_UINT64;
-    if (!encode_2d(&p.tma_a, U8, op.x_codes, kbytes, op.rows, kbytes, BKB, BM, SW128) ||
-        !encode_2d(&p.tma_b, U8, op.w_codes, kbytes, op.n * op.n_groups, kbytes, BKB, BNH, SW128))
-        return cudaErrorInvalidValue;
-    if (fmt_byte_scales(op.fmt)) {
-        const int64_t s_pad = (op.k / fmt_block(op.fmt) + 15) / 16 * 16;
-        p.s4 = (int)(s_pad / 4);
-        const uint32_t nsf = op.fmt == kNVFP4 ? 4 : op.fmt == kMXFP4 ? 2 : 1;
-        const uint64_t atoms_a = (uint64_t)grouped_scale_tiles(op.rows, op.n_groups) * p.s4;
-        const uint64_t atoms_b = (uint64_t)op.n_groups * ((op.n + 127) / 128) * p.s4;
-        if (!encode_2d(&p.tma_sfa, U64, op.x_scales, 64, atoms_a, 512, 64, nsf, NOSW) ||
-            !encode_2d(&p.tma_sfb, U64, op.w_scales, 64, atoms_b, 512, 64, nsf, NOSW))
-            return cudaErrorInvalidValue;
-    }
-    const int esz = op.y_bf16 ? 2 : 4;
-    p.y_tma = (op.n * esz) % 16 == 0;
-    if (p.y_tma && !encode_2d(&p.tma_y, op.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                              op.y, op.n, op.rows, op.n * esz, 32, 32, op.y_bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : SW128))
-        p.y_tma = 0;
-    p.a_row_scale = (const float *)op.x_scales;
-    p.b_row_scale = (const float *)op.w_scales;
-    p.a_ts = op.x_tensor_scale;
-    p.b_ts = op.w_tensor_scales;
-    p.y = op.y;
-    p.m = (int)op.rows;
-    p.n = (int)op.n;
-    p.kbytes = (int)kbytes;
-    p.num_k_tiles = (int)((kbytes + BKB - 1) / BKB);
-    p.y_bf16 = op.y_bf16;
-    p.m_tiles = (int)(op.rows / 256 + (op.rows < op.n_groups ? op.rows : op.n_groups));   // at most
-    p.n_tiles = (int)((op.n + BN - 1) / BN);
-    p.wait_ns = 2000000000ull;   // 2 s
-    p.offsets = op.offsets;
-    p.n_groups = op.n_groups;
-    const int64_t tiles = (int64_t)p.m_tiles * p.n_tiles, pairs = sm_count() / 2;
-    const int grid = 2 * (int)(tiles < pairs ? tiles : pairs);
-    switch (op.fmt) {
-    case kNVFP4: return launch_kind<kKindNVFP4, true>(p, grid, s);
-    case kMXFP4: return launch_kind<kKindMXFP4, true>(p, grid, s);
-    case kMXFP8: return launch_kind<kKindMXFP8, true>(p, grid, s);
-    case kFP8Tensor: return launch_kind<kKindFP8, true>(p, grid, s);
-    case kINT8Row: return launch_kind<kKindINT8, true>(p, grid, s);
-    default: return cudaErrorInvalidValue;
-    }
-}
 
 namespace {
 constexpr unsigned int kErrSelfTest = 64u;

@@ -63,10 +63,14 @@ struct GroupedParams {
     const float *x_row_scale, *w_row_scale;   // INT8
     const float *x_ts, *w_ts;                 // NVFP4, FP8: X's scalar, one per expert
     void *y;
-    int n, kbytes, num_k_tiles, s4, n_tiles, max_tiles, y_bf16, y_vec;
+    int n, kbytes, num_k_tiles, s4, y_bf16, y_vec;
+    int n_tiles, w_tiles;   // feature tiles of an expert, and 128-row tiles of its scales
+    int max_tiles;          // row blocks of all experts at most
     unsigned int *err;
     unsigned long long wait_ns;
 };
+
+// ---- pieces of both kernels; CG: cta_group, 1 or 2
 
 __device__ __forceinline__ void tma_load_2d(const CUtensorMap *map, void *dst, uint64_t *bar, int c0, int c1) {
     asm volatile(
@@ -94,74 +98,183 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                  : "memory");
     return v;
 }
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 template <int F>
 __host__ __device__ constexpr int gn_atoms() { return F == kNVFP4 ? 4 : F == kMXFP4 ? 2 : F == kMXFP8 ? 1 : 0; }
 template <int F>
 __host__ __device__ constexpr int gn_threads() { return 192 + 32 * gn_atoms<F>(); }
+// K-major operands; M / 16 at bit 24 and N / 8 at bit 17 are or-ed in.
 template <int F>
-__host__ __device__ constexpr uint32_t gn_idesc() {   // M = 128, K-major operands; N is or-ed in
-    return (8u << 24) | (F == kNVFP4   ? (1u << 7) | (1u << 10)                 // E2M1, UE4M3 scales
-                         : F == kMXFP4 ? (1u << 7) | (1u << 10) | (1u << 23)    // E2M1, UE8M0 scales
-                         : F == kMXFP8 ? (1u << 23)                             // E4M3, UE8M0 scales
-                         : F == kFP8Tensor ? (1u << 4)                          // E4M3 -> fp32
-                                           : (2u << 4) | (1u << 7) | (1u << 10));   // s8 -> s32
+__host__ __device__ constexpr uint32_t gn_idesc() {
+    return F == kNVFP4       ? (1u << 7) | (1u << 10)                 // E2M1, UE4M3 scales
+           : F == kMXFP4     ? (1u << 7) | (1u << 10) | (1u << 23)    // E2M1, UE8M0 scales
+           : F == kMXFP8     ? (1u << 23)                             // E4M3, UE8M0 scales
+           : F == kFP8Tensor ? (1u << 4)                              // E4M3 -> fp32
+                             : (2u << 4) | (1u << 7) | (1u << 10);    // s8 -> s32
 }
 
-// One 32-byte k-step; sf: the stage's scale columns (8 per atom: W's 4, X's 4).
-template <int F>
-__device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t sf, int ks) {
+#define MXQ_MMA_SCALED(CG, KIND)                                                                                    \
+    asm volatile(                                                                                                   \
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                                           \
+        "tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d),              \
+        "l"(a), "l"(b), "r"(id), "r"(acc), "r"(sa), "r"(sb))
+#define MXQ_MMA_PLAIN(CG, KIND)                                                                                     \
+    asm volatile(                                                                                                   \
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                                           \
+        "tcgen05.mma.cta_group::" CG ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(d),                          \
+        "l"(a), "l"(b), "r"(idesc), "r"(acc))
+
+// One 32-byte k-step.  sf: the stage's scale columns, `pitch` per atom: W's 4,
+// then X's.  An NVFP4 atom serves one k-step, an MXFP4 atom two (scale columns
+// 0-1, then 2-3), an MXFP8 atom four.
+template <int F, int CG>
+__device__ __forceinline__ void mma_step(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t sf,
+                                         uint32_t pitch, int ks) {
+    const int atom = F == kNVFP4 ? ks : F == kMXFP4 ? ks >> 1 : 0;
+    const uint32_t col = F == kMXFP4 ? (uint32_t)(ks & 1) * 2 : F == kMXFP8 ? (uint32_t)ks : 0u;
+    const uint32_t id = idesc | (col << 29) | (col << 4), sa = sf + pitch * atom, sb = sa + 4;
     if (F == kNVFP4) {
-        const uint32_t s = sf + 8 * ks;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(s), "r"(s + 4));
-    } else if (F == kMXFP4) {   // an atom serves two k-steps: its scale columns 0-1, then 2-3
-        const uint32_t s = sf + 8 * (ks >> 1), id = (uint32_t)((ks & 1) * 2);
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc | (id << 29) | (id << 4)), "r"(acc), "r"(s), "r"(s + 4));
-    } else if (F == kMXFP8) {   // an atom serves four
-        const uint32_t id = (uint32_t)ks;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
-            ::"r"(d), "l"(a), "l"(b), "r"(idesc | (id << 29) | (id << 4)), "r"(acc), "r"(sf), "r"(sf + 4));
+        if (CG == 1) MXQ_MMA_SCALED("1", "mxf4nvf4.block_scale.scale_vec::4X");
+        else MXQ_MMA_SCALED("2", "mxf4nvf4.block_scale.scale_vec::4X");
+    } else if (F == kMXFP4) {
+        if (CG == 1) MXQ_MMA_SCALED("1", "mxf4nvf4.block_scale.scale_vec::2X");
+        else MXQ_MMA_SCALED("2", "mxf4nvf4.block_scale.scale_vec::2X");
+    } else if (F == kMXFP8) {
+        if (CG == 1) MXQ_MMA_SCALED("1", "mxf8f6f4.block_scale.scale_vec::1X");
+        else MXQ_MMA_SCALED("2", "mxf8f6f4.block_scale.scale_vec::1X");
     } else if (F == kFP8Tensor) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+        if (CG == 1) MXQ_MMA_PLAIN("1", "f8f6f4");
+        else MXQ_MMA_PLAIN("2", "f8f6f4");
     } else {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc));
+        if (CG == 1) MXQ_MMA_PLAIN("1", "i8");
+        else MXQ_MMA_PLAIN("2", "i8");
     }
 }
 
-// An item: 128 features of an expert times up to 128 of its rows.
+// The box of X (its log2 over 16 rows) that holds `rows` rows.
+__device__ __forceinline__ int box_of(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
+
+// Eight neighbouring values of a row of y from their sums: scaled as
+// mxq_qlinear does it, rounded once, stored.
+template <int F>
+__device__ __forceinline__ void store_row8(const GroupedParams &p, float (&v)[8], int group, int row, int col, float alpha) {
+    if (F == kINT8Row) {
+        const float xs = __ldg(p.x_row_scale + row);
+        const float *ws = p.w_row_scale + (int64_t)group * p.n + col;
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = __fmul_rn(__fmul_rn(v[i], xs), col + i < p.n ? __ldg(ws + i) : 0.0f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = __fmul_rn(v[i], alpha);
+    }
+    const int64_t at = (int64_t)row * p.n + col;
+    const bool whole = p.y_vec && col + 8 <= p.n;
+    if (p.y_bf16) {
+        __nv_bfloat16 *y = reinterpret_cast<__nv_bfloat16 *>(p.y) + at;
+        if (whole) {
+            *reinterpret_cast<uint4 *>(y) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (col + i < p.n) y[i] = __float2bfloat16_rn(v[i]);
+        }
+    } else {
+        float *y = reinterpret_cast<float *>(p.y) + at;
+        if (whole) {
+            reinterpret_cast<float4 *>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4 *>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (col + i < p.n) y[i] = v[i];
+        }
+    }
+}
+// A lane's feature `col` of up to 32 rows from row0 on (`left` of them exist),
+// r[j] the sum of row j: scaled, rounded once and stored without a detour
+// through shared memory.  A row's 32 features of a warp are 64 bytes in bf16,
+// two whole sectors: neighbouring lanes exchange halves so that even lanes
+// hold two features of an even row and odd lanes of the next.
+template <int F>
+__device__ __forceinline__ void store_chunk(const GroupedParams &p, const uint32_t (&r)[32], int row0, int left, int col,
+                                            float alpha, float ws, int lane) {
+    float xs = 0.0f;   // INT8: lane j has row j's scale
+    if (F == kINT8Row && lane < left) xs = __ldg(p.x_row_scale + row0 + lane);
+    auto value = [&](int j) {
+        if (F == kINT8Row) return __fmul_rn(__fmul_rn((float)(int)r[j], __shfl_sync(0xFFFFFFFFu, xs, j)), ws);
+        return __fmul_rn(__uint_as_float(r[j]), alpha);
+    };
+    const bool mine = col < p.n;
+    if (!p.y_bf16) {
+        float *y = reinterpret_cast<float *>(p.y) + (int64_t)row0 * p.n + col;
+#pragma unroll
+        for (int j = 0; j < 32; j++, y += p.n) {
+            const float v = value(j);
+            if (mine && j < left) *y = v;
+        }
+    } else if ((p.n & 1) == 0) {
+        const int odd = lane & 1;
+        const uint32_t pick = odd ? 0x3276u : 0x5410u;
+        __nv_bfloat16 *y = reinterpret_cast<__nv_bfloat16 *>(p.y) + (int64_t)(row0 + odd) * p.n + (col - odd);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2, y += 2 * (int64_t)p.n) {
+            const uint32_t own = pack_bf16x2(value(j), value(j + 1));
+            const uint32_t w = __byte_perm(own, __shfl_xor_sync(0xFFFFFFFFu, own, 1), pick);
+            if (mine && j + odd < left) *reinterpret_cast<uint32_t *>(y) = w;
+        }
+    } else {   // rows that start at odd elements
+        __nv_bfloat16 *y = reinterpret_cast<__nv_bfloat16 *>(p.y) + (int64_t)row0 * p.n + col;
+#pragma unroll
+        for (int j = 0; j < 32; j++, y += p.n) {
+            const float v = value(j);
+            if (mine && j < left) *y = __float2bfloat16_rn(v);
+        }
+    }
+}
+template <int F>
+__device__ __forceinline__ float scale_of(const GroupedParams &p, int group) {
+    return F == kNVFP4 || F == kFP8Tensor ? __fmul_rn(__ldg(p.x_ts), __ldg(p.w_ts + group)) : 1.0f;
+}
+// Whether all 128 epilogue threads say so: they meet at barriers, so they go
+// on together or not at all.
+__device__ __forceinline__ bool all_epilogue(bool ok) {
+    int all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, 2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((int)ok)
+        : "memory");
+    return all != 0;
+}
+
+// ---- few rows per expert
+
+// An item: a feature tile of an expert times a block of 128 (or, WIDE, 256) of
+// its rows.  An expert's blocks of one feature tile are neighbours.
 struct Item {
     int group, tile_n, row0, n_rows, sf_tile;
 };
+template <bool WIDE>
 __device__ __forceinline__ Item item_at(const Groups &g, int n_groups, int n_tiles, int item) {
+    const int *before = WIDE ? g.wide : g.tile;
     const int key = item / n_tiles;   // the item's row block, counted over all groups
     int lo = 0, hi = n_groups;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (g.tile[mid] <= key) lo = mid;
+        if (before[mid] <= key) lo = mid;
         else hi = mid;
     }
-    const int blocks = g.tile[lo + 1] - g.tile[lo], within = item - g.tile[lo] * n_tiles;
+    constexpr int R = WIDE ? 256 : 128;
+    const int blocks = before[lo + 1] - before[lo], within = item - before[lo] * n_tiles;
     Item it;
     it.group = lo;
     it.tile_n = within / blocks;
     const int block = within - it.tile_n * blocks;
-    it.row0 = g.off[lo] + block * 128;
+    it.row0 = g.off[lo] + block * R;
     const int left = g.off[lo + 1] - it.row0;
-    it.n_rows = left < 128 ? left : 128;
-    it.sf_tile = g.tile[lo] + block;
+    it.n_rows = left < R ? left : R;
+    it.sf_tile = g.tile[lo] + block * (R / 128);
     return it;
 }
 
@@ -231,8 +344,8 @@ __global__ void __launch_bounds__(gn_threads<F>(), 1) k_gemm_grouped_few(const _
         if (lane == 0) {
             int it = 0;
             for (int item = cid; item < items && !*abort_flag; item += ncl) {
-                const Item w = item_at(groups, p.n_groups, p.n_tiles, item);
-                const int box = w.n_rows <= 16 ? 0 : w.n_rows <= 32 ? 1 : w.n_rows <= 64 ? 2 : 3;
+                const Item w = item_at<false>(groups, p.n_groups, p.n_tiles, item);
+                const int box = box_of(w.n_rows);
                 const uint32_t bytes = GN_W + ((16u << box) * 128u) + NSF * 1024u;
                 for (int kt = kt0; kt < kt1; kt++, it++) {
                     const int s = it % GN_STAGES;
@@ -246,7 +359,7 @@ __global__ void __launch_bounds__(gn_threads<F>(), 1) k_gemm_grouped_few(const _
                     tma_load_2d(&p.w, sw, full + s, kt * 128, w.group * p.n + w.tile_n * 128);
                     tma_load_2d(&p.x[box], sw + GN_W, full + s, kt * 128, w.row0);
                     if (NSF) {
-                        tma_load_2d(&p.sfw, sw + GN_W + GN_X, full + s, 0, (w.group * p.n_tiles + w.tile_n) * p.s4 + kt * NSF);
+                        tma_load_2d(&p.sfw, sw + GN_W + GN_X, full + s, 0, (w.group * p.w_tiles + w.tile_n) * p.s4 + kt * NSF);
                         tma_load_2d(&p.sfx, sw + GN_W + GN_X + GN_SF, full + s, 0, w.sf_tile * p.s4 + kt * NSF);
                     }
                 }
@@ -260,8 +373,8 @@ __global__ void __launch_bounds__(gn_threads<F>(), 1) k_gemm_grouped_few(const _
             int it = 0, count = 0;
             const uint64_t ad0 = sdesc_sw128(smem), bd0 = sdesc_sw128(smem + GN_W);
             for (int item = cid; item < items && !*abort_flag; item += ncl, count++) {
-                const Item w = item_at(groups, p.n_groups, p.n_tiles, item);
-                const uint32_t idesc = gn_idesc<F>() | ((uint32_t)((w.n_rows + 15) >> 4) << 18);   // N / 8 at bit 17
+                const Item w = item_at<false>(groups, p.n_groups, p.n_tiles, item);
+                const uint32_t idesc = gn_idesc<F>() | (8u << 24) | ((uint32_t)((w.n_rows + 15) >> 4) << 18);
                 const int st = count & 1;
                 const uint32_t acc = tmem + 128u * st;
                 bool ok = mbar_wait_spin(acce + st, ((count >> 1) & 1) ^ 1, p.wait_ns);
@@ -277,7 +390,7 @@ __global__ void __launch_bounds__(gn_threads<F>(), 1) k_gemm_grouped_few(const _
 #pragma unroll
                     for (int ks = 0; ks < 4; ks++)
                         if (ks < nks)
-                            mma_step<F>(acc, ad0 + off + 2 * ks, bd0 + off + 2 * ks, idesc, kt > kt0 || ks > 0, sft, ks);
+                            mma_step<F, 1>(acc, ad0 + off + 2 * ks, bd0 + off + 2 * ks, idesc, kt > kt0 || ks > 0, sft, 8, ks);
                     tc_commit(empty + s);
                 }
                 if (!ok) {
@@ -327,25 +440,19 @@ __global__ void __launch_bounds__(gn_threads<F>(), 1) k_gemm_grouped_few(const _
         uint32_t chunks = 0;   // staging rounds done
         bool ok = true;
         for (int item = cid; item < items; item += ncl, count++) {
-            const Item w = item_at(groups, p.n_groups, p.n_tiles, item);
+            const Item w = item_at<false>(groups, p.n_groups, p.n_tiles, item);
             const int st = count & 1;
             ok = ok && !*abort_flag && mbar_wait(accf + st, (count >> 1) & 1, p.wait_ns);
-            // all 128 threads go on or none does: they meet at barriers below
-            int all;
-            asm volatile(
-                "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, 2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
-                : "=r"(all)
-                : "r"((int)ok)
-                : "memory");
-            if (!all) {
+            if (!all_epilogue(ok)) {
                 if (!ok && !*abort_flag) atomicOr(p.err, kErrGrouped);
                 *abort_flag = 1;
                 break;
             }
             tc_fence_after();
-            float alpha = 1.0f;
-            if (F == kNVFP4 || F == kFP8Tensor) alpha = __fmul_rn(__ldg(p.x_ts), __ldg(p.w_ts + w.group));
+            const float alpha = scale_of<F>(p, w.group);
             const int n0 = w.tile_n * 128, n_chunks = (w.n_rows + 31) >> 5;
+            const float ws =
+                F == kINT8Row && n0 + feature < p.n ? __ldg(p.w_row_scale + (int64_t)w.group * p.n + n0 + feature) : 0.0f;
             for (int c = 0; c < n_chunks; c++, chunks++) {
                 uint32_t r[32];
                 __syncwarp();
@@ -355,87 +462,43 @@ __global__ void __launch_bounds__(gn_threads<F>(), 1) k_gemm_grouped_few(const _
                     __syncwarp();
                     if (lane == 0) mbar_arrive_local_relaxed(acce + st);
                 }
-                // the staging of the round before has been read, here and by the cluster
-                if (split == 1) epilogue_sync();
-                else if (chunks > 0 && ok) ok = mbar_wait<true>(freed, (chunks - 1) & 1, p.wait_ns);
+                if (split == 1) {
+                    store_chunk<F>(p, r, w.row0 + c * 32, w.n_rows - c * 32, n0 + feature, alpha, ws, lane);
+                    continue;
+                }
+                // the staging of the round before has been read by the cluster
+                if (chunks > 0 && ok) ok = mbar_wait<true>(freed, (chunks - 1) & 1, p.wait_ns);
 #pragma unroll
                 for (int j = 0; j < 32; j++) staging[j * 128 + feature] = r[j];
-                if (split == 1) {
-                    epilogue_sync();
-                } else {
-                    __syncwarp();
-                    if (lane < (int)split) mbar_arrive_remote(map_to_rank(ready, lane));
-                    if (ok) ok = mbar_wait<true>(ready, chunks & 1, p.wait_ns);
-                }
+                __syncwarp();
+                if (lane < (int)split) mbar_arrive_remote(map_to_rank(ready, lane));
+                if (ok) ok = mbar_wait<true>(ready, chunks & 1, p.wait_ns);
                 // rows rank * 32 / split .. of the chunk, 8 features per thread
                 const int per = 32 / (int)split, v8 = et & 15;
                 for (int j = et >> 4; j < per && ok; j += 8) {
                     const int jr = (int)rank * per + j, row = w.row0 + c * 32 + jr;
                     if (c * 32 + jr >= w.n_rows) break;
                     const uint32_t *src = staging + jr * 128 + v8 * 8;
-                    float v[8];
-                    if (split == 1) {
-                        const uint4 a = *reinterpret_cast<const uint4 *>(src), b = *reinterpret_cast<const uint4 *>(src + 4);
-                        const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                    float v[8] = {};
+                    int vi[8] = {};
+                    for (uint32_t s = 0; s < split; s++) {
+                        const uint32_t at = map_to_rank(src, s);
+                        const float4 a = ld_cluster_f4(at), b = ld_cluster_f4(at + 16);
+                        const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-                        for (int i = 0; i < 8; i++) v[i] = F == kINT8Row ? (float)(int)u[i] : __uint_as_float(u[i]);
-                    } else {
-                        int vi[8] = {};
-#pragma unroll
-                        for (int i = 0; i < 8; i++) v[i] = 0.0f;
-                        for (uint32_t s = 0; s < split; s++) {
-                            const uint32_t at = map_to_rank(src, s);
-                            const float4 a = ld_cluster_f4(at), b = ld_cluster_f4(at + 16);
-                            const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                            for (int i = 0; i < 8; i++) {
-                                if (F == kINT8Row) vi[i] += __float_as_int(u[i]);
-                                else v[i] = __fadd_rn(v[i], u[i]);
-                            }
-                        }
-                        if (F == kINT8Row) {
-#pragma unroll
-                            for (int i = 0; i < 8; i++) v[i] = (float)vi[i];
+                        for (int i = 0; i < 8; i++) {
+                            if (F == kINT8Row) vi[i] += __float_as_int(u[i]);
+                            else v[i] = __fadd_rn(v[i], u[i]);
                         }
                     }
-                    const int col = n0 + v8 * 8;
                     if (F == kINT8Row) {
-                        const float xs = __ldg(p.x_row_scale + row);
-                        const float *ws = p.w_row_scale + (int64_t)w.group * p.n + col;
 #pragma unroll
-                        for (int i = 0; i < 8; i++)
-                            v[i] = __fmul_rn(__fmul_rn(v[i], xs), col + i < p.n ? __ldg(ws + i) : 0.0f);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; i++) v[i] = __fmul_rn(v[i], alpha);
+                        for (int i = 0; i < 8; i++) v[i] = (float)vi[i];
                     }
-                    const int64_t at = (int64_t)row * p.n + col;
-                    if (p.y_bf16) {
-                        __nv_bfloat16 *y = reinterpret_cast<__nv_bfloat16 *>(p.y) + at;
-                        if (p.y_vec && col + 8 <= p.n) {
-                            *reinterpret_cast<uint4 *>(y) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; i++)
-                                if (col + i < p.n) y[i] = __float2bfloat16_rn(v[i]);
-                        }
-                    } else {
-                        float *y = reinterpret_cast<float *>(p.y) + at;
-                        if (p.y_vec && col + 8 <= p.n) {
-                            reinterpret_cast<float4 *>(y)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            reinterpret_cast<float4 *>(y)[1] = make_float4(v[4], v[5], v[6], v[7]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; i++)
-                                if (col + i < p.n) y[i] = v[i];
-                        }
-                    }
+                    store_row8<F>(p, v, w.group, row, n0 + v8 * 8, alpha);
                 }
-                if (split > 1) {
-                    __syncwarp();
-                    if (lane < (int)split) mbar_arrive_remote(map_to_rank(freed, lane));
-                }
+                __syncwarp();
+                if (lane < (int)split) mbar_arrive_remote(map_to_rank(freed, lane));
             }
             if (!ok) {
                 if (!*abort_flag) atomicOr(p.err, kErrGrouped);
@@ -451,6 +514,289 @@ __global__ void __launch_bounds__(gn_threads<F>(), 1) k_gemm_grouped_few(const _
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(GN_TMEM_COLS));
+    }
+}
+
+// ---- many rows per expert
+//
+// A pair of CTAs (cta_group::2) computes 256 features x up to 256 rows: each
+// stages its 128 weight rows and half of the block's rows of X, holds the
+// scales of its weight rows and of all rows of X, and its 128 features x N
+// accumulator.  N is the block's rows rounded up to 32, so a ragged block costs
+// what it has, in MMA time and in loads.  Warps as in the few-rows kernel; the
+// first CTA's MMA and scale threads serve both.  The accumulator stages lie at
+// columns 0 and GP_ACC1 and share columns with a full block (two of 256 do not
+// fit beside the scales): the epilogue takes the shared chunks to registers
+// first and releases them.
+
+constexpr int GP_STAGES = 5;
+constexpr int GP_SF = 6144;   // W's atoms at 0, X's first 128 rows' at 2048, the others' at 4096
+constexpr int GP_STAGE = GN_W + GN_X + GP_SF;
+constexpr int GP_SMEM = GP_STAGES * GP_STAGE + (int)sizeof(Groups) + 256 + 1024;
+static_assert(GP_SMEM <= 227 * 1024, "shared memory budget");
+constexpr uint32_t GP_SF_PITCH = 12, GP_SF_COLS = 48, GP_SF_GROUPS = 2;   // per atom, per stage; stages in TMEM at a time
+template <int F>
+__host__ __device__ constexpr uint32_t gp_acc1() { return gn_atoms<F>() ? 160u : 256u; }
+constexpr uint32_t GP_TMEM_SF = 512 - GP_SF_GROUPS * GP_SF_COLS;
+static_assert(160 + 256 <= GP_TMEM_SF, "TMEM budget");
+
+__device__ __forceinline__ void tma_load_pair(const CUtensorMap *map, void *dst, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs once the issued MMAs complete.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair_self(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tc_cp_pair(uint32_t taddr, uint64_t sdesc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+template <int F>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gn_threads<F>(), 1)
+    k_gemm_grouped_many(const __grid_constant__ GroupedParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + GP_STAGES * GP_STAGE);   // (used in the first CTA)
+    uint64_t *empty = full + GP_STAGES;
+    uint64_t *accf = empty + GP_STAGES;      // [2] accumulator stage full
+    uint64_t *acce = accf + 2;               // [2] drained (first CTA)
+    uint64_t *ovlf = acce + 2;               // shared columns drained (first CTA)
+    uint64_t *drain = ovlf + 1;
+    uint64_t *sfready = drain + 1;           // [GP_STAGES] a stage's scales in TMEM (first CTA)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sfready + GP_STAGES);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    Groups &groups = *reinterpret_cast<Groups *>(smem + GP_STAGES * GP_STAGE + 256);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int cid = (int)cluster_id(), ncl = (int)cluster_count();
+    constexpr int NSF = gn_atoms<F>();
+
+    if (warp == 0 && lane < 7) {
+        const CUtensorMap *m = lane < 4 ? p.x + lane : lane == 4 ? &p.w : lane == 5 ? &p.sfw : &p.sfx;
+        if (lane < 5 || NSF) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < GP_STAGES; s++) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+            mbar_init(sfready + s, NSF ? NSF : 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(accf + i, 1);
+            mbar_init(acce + i, 8);   // 4 epilogue warps x 2 CTAs
+        }
+        mbar_init(ovlf, 8);
+        mbar_init(drain, 1 + NSF);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(GN_TMEM_COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+    load_groups(groups, p.offsets, p.n_groups, p.rows, blockIdx.x == 0 ? p.err : nullptr);
+    const int blocks = groups.wide[p.n_groups];   // above max_tiles only for offsets out of order
+    const int items = (blocks < p.max_tiles ? blocks : p.max_tiles) * p.n_tiles;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (int item = cid; item < items && !*abort_flag; item += ncl) {
+                const Item w = item_at<true>(groups, p.n_groups, p.n_tiles, item);
+                const int half = ((w.n_rows + 31) >> 5) << 4;   // rows of X in each CTA
+                const int box = box_of(half);
+                const bool hi = w.n_rows > 128;                 // X's second scale tile
+                const uint32_t bytes = 2u * (GN_W + (2048u << box)) + NSF * 512u * 2u * (hi ? 3u : 2u);
+                const int wrow = w.group * p.n + w.tile_n * 256 + (int)rank * 128, xrow = w.row0 + (int)rank * half;
+                const int wsf = w.group * p.w_tiles + w.tile_n * 2 + (int)rank;
+                for (int kt = 0; kt < p.num_k_tiles; kt++, it++) {
+                    const int s = it % GP_STAGES;
+                    if (!mbar_wait(empty + s, ((it / GP_STAGES) & 1) ^ 1, p.wait_ns)) {
+                        atomicOr(p.err, kErrGrouped);
+                        *abort_flag = 1;
+                    }
+                    if (*abort_flag) break;
+                    uint8_t *sw = smem + s * GP_STAGE, *sf = sw + GN_W + GN_X;
+                    const uint32_t bar = map_to_rank(full + s, 0);
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
+                    tma_load_pair(&p.w, sw, bar, kt * 128, wrow);
+                    tma_load_pair(&p.x[box], sw + GN_W, bar, kt * 128, xrow);
+                    if (NSF) {
+                        tma_load_pair(&p.sfw, sf, bar, 0, wsf * p.s4 + kt * NSF);
+                        tma_load_pair(&p.sfx, sf + 2048, bar, 0, w.sf_tile * p.s4 + kt * NSF);
+                        if (hi) tma_load_pair(&p.sfx, sf + 4096, bar, 0, (w.sf_tile + 1) * p.s4 + kt * NSF);
+                    }
+                }
+            }
+            if (*abort_flag && rank == 0)   // wait (bounded) for the loads that may still be in flight
+                for (int i = (it > GP_STAGES ? it - GP_STAGES : 0); i < it; i++)
+                    mbar_wait(full + (i % GP_STAGES), (i / GP_STAGES) & 1, p.wait_ns);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int it = 0, count = 0, s = 0;
+            uint32_t ph = 0;
+            const uint64_t ad0 = sdesc_sw128(smem), bd0 = sdesc_sw128(smem + GN_W);
+            for (int item = cid; item < items && !*abort_flag; item += ncl, count++) {
+                const Item w = item_at<true>(groups, p.n_groups, p.n_tiles, item);
+                const uint32_t idesc = gn_idesc<F>() | (16u << 24) | ((uint32_t)((w.n_rows + 31) >> 5) << 19);
+                const int st = count & 1;
+                const uint32_t acc = tmem + (st ? gp_acc1<F>() : 0u);
+                // this stage drained (item count - 2) and the shared columns (item count - 1), in both CTAs
+                bool ok = mbar_wait_spin<true>(acce + st, ((count >> 1) & 1) ^ 1, p.wait_ns);
+                if (NSF && ok && count > 0) ok = mbar_wait_spin<true>(ovlf, (count - 1) & 1, p.wait_ns);
+                tc_fence_after();
+                for (int kt = 0; kt < p.num_k_tiles && ok && !*abort_flag; kt++, it++) {
+                    ok = mbar_wait_spin(NSF ? sfready + s : full + s, ph, p.wait_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sft = tmem + GP_TMEM_SF + GP_SF_COLS * ((uint32_t)it % GP_SF_GROUPS);
+                    const int left = (p.kbytes - kt * 128) >> 5;
+                    const uint64_t off = (uint64_t)(s * (GP_STAGE >> 4));
+#pragma unroll
+                    for (int ks = 0; ks < 4; ks++)
+                        if (ks < left)
+                            mma_step<F, 2>(acc, ad0 + off + 2 * ks, bd0 + off + 2 * ks, idesc, (kt | ks) != 0, sft, GP_SF_PITCH, ks);
+                    tc_commit_pair(empty + s);
+                    if (++s == GP_STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) {
+                    atomicOr(p.err, kErrGrouped);
+                    *abort_flag = 1;
+                }
+                if (*abort_flag) break;
+                tc_commit_pair(accf + st);
+            }
+            if (*abort_flag) {   // what is in flight lands before the TMEM is freed
+                tc_commit_pair_self(drain);
+                mbar_wait(drain, 0, p.wait_ns);
+            }
+        }
+    } else if (warp >= 6) {
+        const int atom = warp - 6;
+        if (NSF && lane == 0 && rank == 0) {
+            int it = 0;
+            for (int item = cid; item < items && !*abort_flag; item += ncl) {
+                const bool hi = item_at<true>(groups, p.n_groups, p.n_tiles, item).n_rows > 128;
+                for (int kt = 0; kt < p.num_k_tiles; kt++, it++) {
+                    const int s = it % GP_STAGES;
+                    bool ok = mbar_wait(full + s, (it / GP_STAGES) & 1, p.wait_ns);
+                    // these columns were last read by the MMAs of k-tile it - GP_SF_GROUPS
+                    const int prev = it - (int)GP_SF_GROUPS;
+                    if (ok && prev >= 0) ok = mbar_wait(empty + prev % GP_STAGES, (prev / GP_STAGES) & 1, p.wait_ns);
+                    if (!ok) {
+                        atomicOr(p.err, kErrGrouped);
+                        *abort_flag = 1;
+                    }
+                    if (*abort_flag) break;
+                    tc_fence_after();
+                    if (atom * (4 / (NSF ? NSF : 1)) * 32 < p.kbytes - kt * 128) {
+                        const uint8_t *sf = smem + s * GP_STAGE + GN_W + GN_X + 512 * atom;
+                        const uint32_t to = tmem + GP_TMEM_SF + GP_SF_COLS * ((uint32_t)it % GP_SF_GROUPS) + GP_SF_PITCH * atom;
+                        tc_cp_pair(to, sdesc_atom(sf));
+                        tc_cp_pair(to + 4, sdesc_atom(sf + 2048));
+                        if (hi) tc_cp_pair(to + 8, sdesc_atom(sf + 4096));
+                    }
+                    tc_commit_pair_self(sfready + s);
+                }
+            }
+            if (*abort_flag) {
+                tc_commit_pair_self(drain);
+                mbar_wait(drain, 0, p.wait_ns);
+            }
+        }
+    } else {
+        const int q = warp & 3, feature = q * 32 + lane;   // TMEM lane quarter and lane
+        const uint32_t ovl_to = map_to_rank(ovlf, 0), acce_to = map_to_rank(acce, 0);   // acce + 1: 8 bytes on
+        int count = 0;
+        for (int item = cid; item < items; item += ncl, count++) {
+            const Item w = item_at<true>(groups, p.n_groups, p.n_tiles, item);
+            const int st = count & 1;
+            const bool ok = !*abort_flag && mbar_wait(accf + st, (count >> 1) & 1, p.wait_ns);
+            if (!all_epilogue(ok)) {
+                if (!ok && !*abort_flag) atomicOr(p.err, kErrGrouped);
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after();
+            const float alpha = scale_of<F>(p, w.group);
+            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (st ? gp_acc1<F>() : 0u);
+            const int col = w.tile_n * 256 + (int)rank * 128 + feature, n_chunks = (w.n_rows + 31) >> 5;
+            const float ws = F == kINT8Row && col < p.n ? __ldg(p.w_row_scale + (int64_t)w.group * p.n + col) : 0.0f;
+            auto process = [&](int c, const uint32_t (&r)[32]) {   // 32 rows of the block
+                store_chunk<F>(p, r, w.row0 + c * 32, w.n_rows - c * 32, col, alpha, ws, lane);
+            };
+            // chunks [first, first + shared) lie in columns that the other stage uses too
+            constexpr int kShared = NSF ? 3 : 0;   // columns 160 .. 255
+            int first = 0, shared = 0;
+            if constexpr (kShared > 0) {
+                first = st ? 0 : 5;
+                shared = n_chunks - first < 0 ? 0 : n_chunks - first < kShared ? n_chunks - first : kShared;
+                uint32_t ro[kShared][32];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kShared; i++)
+                    if (i < shared) tmem_ld_32x32b_x32_async(acc + 32u * (first + i), ro[i]);
+                tmem_ld_wait(ro[kShared - 1]);
+#pragma unroll
+                for (int i = 0; i + 1 < kShared; i++) tmem_reg_tie(ro[i]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_relaxed(ovl_to);
+#pragma unroll
+                for (int i = 0; i < kShared; i++)
+                    if (i < shared) process(first + i, ro[i]);
+            }
+            const int others = n_chunks - shared;
+            if (others == 0) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_relaxed(acce_to + 8u * st);
+            }
+#pragma unroll 1
+            for (int i = 0; i < others; i++) {
+                const int c = st ? shared + i : i;
+                uint32_t r[32];
+                __syncwarp();
+                tmem_ld_32x32b_x32(acc + 32u * c, r);
+                if (i == others - 1) {   // the whole stage is drained
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote_relaxed(acce_to + 8u * st);
+                }
+                process(c, r);
+            }
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(GN_TMEM_COLS));
     }
 }
 
@@ -477,26 +823,66 @@ cudaError_t launch_few(const GroupedParams &p, int clusters, int split, cudaStre
     return cudaLaunchKernelEx(&cfg, k_gemm_grouped_few<F>, p);
 }
 
+template <int F>
+cudaError_t launch_many(const GroupedParams &p, int clusters, cudaStream_t s) {
+    static PerDeviceOnce smem_opt_in;
+    cudaError_t e = smem_opt_in.run([] {
+        return cudaFuncSetAttribute(k_gemm_grouped_many<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+    cfg.blockDim = dim3(gn_threads<F>(), 1, 1);
+    cfg.dynamicSmemBytes = GP_SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1] = {pdl_attribute()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_gemm_grouped_many<F>, p);
+}
+
+// The host knows the rows of all experts together, not of each: their mean
+// decides between the kernels.
+template <int F>
+cudaError_t launch_fmt(GroupedParams &p, const GroupedOperands &op, cudaStream_t s) {
+    const int sms = sm_count();
+    const int64_t ragged = op.rows < op.n_groups ? op.rows : op.n_groups;   // blocks that may be partly filled
+    if (op.rows > 64 * (int64_t)op.n_groups) {
+        p.n_tiles = (int)((op.n + 255) / 256);
+        p.max_tiles = (int)(op.rows / 256 + ragged);
+        const int64_t items = (int64_t)p.max_tiles * p.n_tiles;
+        return launch_many<F>(p, (int)(items < sms / 2 ? items : sms / 2), s);
+    }
+    p.n_tiles = p.w_tiles;
+    p.max_tiles = (int)(op.rows / 128 + ragged);
+    // K is split while the items at most leave SMs idle and every CTA keeps at least two stages
+    const int64_t items = (int64_t)p.max_tiles * p.n_tiles;
+    int split = 1;
+    while (split < 8 && items * split * 2 <= sms && p.num_k_tiles >= split * 4) split *= 2;
+    return launch_few<F>(p, (int)(items < sms / split ? items : sms / split), split, s);
+}
+
 }  // namespace
 
-static cudaError_t launch_qlinear_grouped_few(const GroupedOperands &op, cudaStream_t s) {
+cudaError_t launch_qlinear_grouped(const GroupedOperands &op, cudaStream_t s) {
     GroupedParams p;
     memset(&p, 0, sizeof(p));
     const int64_t kbytes = fmt_is4(op.fmt) ? op.k / 2 : op.k;
     const auto SW128 = CU_TENSOR_MAP_SWIZZLE_128B, NOSW = CU_TENSOR_MAP_SWIZZLE_NONE;
     const auto U8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, U64 = CU_TENSOR_MAP_DATA_TYPE_UINT64;
-    p.n_tiles = (int)((op.n + 127) / 128);
-    p.max_tiles = (int)grouped_scale_tiles(op.rows, op.n_groups);
     if (!encode_2d(&p.w, U8, op.w_codes, kbytes, op.n * op.n_groups, kbytes, 128, 128, SW128)) return cudaErrorInvalidValue;
     for (int i = 0; i < 4; i++)
         if (!encode_2d(&p.x[i], U8, op.x_codes, kbytes, op.rows, kbytes, 128, 16u << i, SW128)) return cudaErrorInvalidValue;
+    p.w_tiles = (int)((op.n + 127) / 128);
     if (fmt_byte_scales(op.fmt)) {
         // scale atoms as rows of 64 x 8 bytes
         const int64_t s_pad = (op.k / fmt_block(op.fmt) + 15) / 16 * 16;
         p.s4 = (int)(s_pad / 4);
         const uint32_t atoms = op.fmt == kNVFP4 ? 4 : op.fmt == kMXFP4 ? 2 : 1;
-        if (!encode_2d(&p.sfw, U64, op.w_scales, 64, (uint64_t)op.n_groups * p.n_tiles * p.s4, 512, 64, atoms, NOSW) ||
-            !encode_2d(&p.sfx, U64, op.x_scales, 64, (uint64_t)p.max_tiles * p.s4, 512, 64, atoms, NOSW))
+        const uint64_t w_atoms = (uint64_t)op.n_groups * p.w_tiles * p.s4;
+        const uint64_t x_atoms = (uint64_t)grouped_scale_tiles(op.rows, op.n_groups) * p.s4;
+        if (!encode_2d(&p.sfw, U64, op.w_scales, 64, w_atoms, 512, 64, atoms, NOSW) ||
+            !encode_2d(&p.sfx, U64, op.x_scales, 64, x_atoms, 512, 64, atoms, NOSW))
             return cudaErrorInvalidValue;
     }
     p.offsets = op.offsets;
@@ -513,30 +899,16 @@ static cudaError_t launch_qlinear_grouped_few(const GroupedOperands &op, cudaStr
     p.y_bf16 = op.y_bf16;
     p.y_vec = op.n % 8 == 0 && (reinterpret_cast<uintptr_t>(op.y) & 15u) == 0;
     p.wait_ns = 2000000000ull;   // 2 s
-    cudaError_t e = error_word_address(&p.err);
+    const cudaError_t e = error_word_address(&p.err);
     if (e != cudaSuccess) return e;
-    const int sms = sm_count();
-    // K is split while the items at most (the host does not know the rows of each expert) leave SMs idle and every
-    // CTA keeps at least two stages
-    const int64_t items = (int64_t)p.max_tiles * p.n_tiles;
-    int split = 1;
-    while (split < 8 && items * split * 2 <= sms && p.num_k_tiles >= split * 4) split *= 2;
-    const int clusters = (int)(items < sms / split ? items : sms / split);
     switch (op.fmt) {
-    case kNVFP4: return launch_few<kNVFP4>(p, clusters, split, s);
-    case kMXFP4: return launch_few<kMXFP4>(p, clusters, split, s);
-    case kMXFP8: return launch_few<kMXFP8>(p, clusters, split, s);
-    case kFP8Tensor: return launch_few<kFP8Tensor>(p, clusters, split, s);
-    case kINT8Row: return launch_few<kINT8Row>(p, clusters, split, s);
+    case kNVFP4: return launch_fmt<kNVFP4>(p, op, s);
+    case kMXFP4: return launch_fmt<kMXFP4>(p, op, s);
+    case kMXFP8: return launch_fmt<kMXFP8>(p, op, s);
+    case kFP8Tensor: return launch_fmt<kFP8Tensor>(p, op, s);
+    case kINT8Row: return launch_fmt<kINT8Row>(p, op, s);
     default: return cudaErrorInvalidValue;
     }
-}
-
-// The host knows the rows of all experts together, not of each: their mean
-// decides.
-cudaError_t launch_qlinear_grouped(const GroupedOperands &op, cudaStream_t s) {
-    if (op.rows > 64 * (int64_t)op.n_groups) return launch_qlinear_grouped_many(op, s);
-    return launch_qlinear_grouped_few(op, s);
 }
 
 }  // namespace mxq

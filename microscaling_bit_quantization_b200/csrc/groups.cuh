@@ -26,6 +26,7 @@ __device__ __forceinline__ int clamp_row(int o, int64_t rows) {
 struct Groups {
     int off[kMaxGroups + 1];
     int tile[kMaxGroups + 1];   // 128-row scale tiles before each group
+    int wide[kMaxGroups + 1];   // blocks of 256 rows before each group
 };
 
 // Fills `g` (all threads of the block call this); a table that had to be
@@ -39,21 +40,31 @@ __device__ __forceinline__ void load_groups(Groups &g, const int32_t *offsets, i
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
-        int carry = 0;
+        int carry = 0, carry2 = 0;
         for (int b = 0; b < n; b += 32) {
             const int e = b + lane;
             const int rows_e = e < n ? g.off[e + 1] - g.off[e] : 0;
-            const int t = rows_e > 0 ? (rows_e + 127) >> 7 : 0;
-            int s = t;
+            const int t = rows_e > 0 ? (rows_e + 127) >> 7 : 0, w = (t + 1) >> 1;
+            int s = t, s2 = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, s, o);
-                if (lane >= o) s += v;
+                const int v = __shfl_up_sync(0xFFFFFFFFu, s, o), v2 = __shfl_up_sync(0xFFFFFFFFu, s2, o);
+                if (lane >= o) {
+                    s += v;
+                    s2 += v2;
+                }
             }
-            if (e < n) g.tile[e] = carry + s - t;
+            if (e < n) {
+                g.tile[e] = carry + s - t;
+                g.wide[e] = carry2 + s2 - w;
+            }
             carry += __shfl_sync(0xFFFFFFFFu, s, 31);
+            carry2 += __shfl_sync(0xFFFFFFFFu, s2, 31);
         }
-        if (lane == 0) g.tile[n] = carry;
+        if (lane == 0) {
+            g.tile[n] = carry;
+            g.wide[n] = carry2;
+        }
     }
     __syncthreads();
 }

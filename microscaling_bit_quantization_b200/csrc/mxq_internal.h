@@ -196,10 +196,10 @@ cudaError_t launch_mixed_scatter(const void *const ybuf[3], const int64_t n_grou
                                  const int32_t *group_index, void *y, bool y_bf16, int64_t m, int64_t n,
                                  cudaStream_t s);
 
-// ---- rows in expert order (experts.cu, gemm_grouped.cu, gemm.cu)
-// Groups (experts) of a grouped call, and rows in expert order: the wide
-// product kernel keeps a 16-bit count of 128-row tiles per group in the
-// shared memory its ring leaves, and rows / 128 + groups must fit it.
+// ---- rows in expert order (experts.cu, gemm_grouped.cu)
+// Groups (experts) of a grouped call, and rows in expert order at most: the
+// kernels keep a table of the groups in shared memory and count rows and tiles
+// in 31 bits.
 constexpr int kMaxGroups = 512;
 constexpr int64_t kMaxGroupedRows = (int64_t)1 << 22;
 constexpr int kPlanMaxBlocks = 128;
@@ -230,8 +230,7 @@ struct GroupedOperands {
     void *y;
     bool y_bf16;
 };
-cudaError_t launch_qlinear_grouped(const GroupedOperands &op, cudaStream_t s);        // gemm_grouped.cu: the choice
-cudaError_t launch_qlinear_grouped_many(const GroupedOperands &op, cudaStream_t s);   // gemm.cu
+cudaError_t launch_qlinear_grouped(const GroupedOperands &op, cudaStream_t s);
 // q/k head norm and position rotation (heads.cu); fmt < 0: outputs in the
 // input's type, else codes and scales in that format.
 struct HeadArgs {
