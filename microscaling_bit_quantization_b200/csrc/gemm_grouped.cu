@@ -1,34 +1,30 @@
 // gemm_grouped.cu -- products of rows in expert order with their expert's
-// low-bit weight, for few rows per expert (a decode step, a small batch): the
-// memory-bound end, where every busy expert's weight has to be read once and
-// the tensor cores have time to spare.  gemm.cu's grouped kernel takes over
-// where experts have many rows.
+// low-bit weight on tcgen05 tensor cores.
 //
-// The product is turned round: the weight is the 128-row operand of a
-// cta_group::1 MMA and the rows of one expert are its N = 16 .. 128 columns,
-// N being the expert's rows rounded up to 16 (up to 128 at a time).  So a
-// tile reads no more of X than there is, and the ring's bytes are nearly all
-// weight.  Per CTA:
-//   warp 0      TMA producer into a 5-stage ring: 128 weight rows x 128 bytes,
-//               16 / 32 / 64 / 128 rows of X by the box that fits, scale atoms
+// The product is turned round: the weight gives the MMA's M rows and the rows
+// of one expert its N columns, N being what the expert has (rounded up to 16 or
+// 32).  So a ragged group costs its rows and no more, in MMA time and in the
+// bytes of X that a stage loads, and with few rows per expert (a decode step)
+// the ring's bytes are nearly all weight, which has to be read once anyway.
+//
+// Two kernels, chosen on the host from the sizes it knows:
+//   k_gemm_grouped_pair   CTA pairs (cta_group::2), 256 features x up to 128 or
+//                         256 rows, persistent over (expert, features, rows)
+//   k_gemm_grouped_split  where there are so few such items that SMs would
+//                         idle: K split over a cluster of 2 or 4 CTAs
+// Warps of both:
+//   warp 0      TMA producer into a ring of K stages: 128 weight rows x 128
+//               bytes, the box of 16 / 32 / 64 / 128 rows of X that fits, the
+//               scale atoms of both
 //   warp 1      TMEM allocation and the thread that issues the MMAs
-//   warps 2-5   epilogue: TMEM -> shared staging [32 rows][128 features] ->
-//               scaled rows of y
-//   warps 6-    a thread per scale atom of a stage that copies it (X's and
-//               W's) to TMEM, each stage having its own columns: a tcgen05.cp
-//               holds up the thread that issues it, and NVFP4 has eight a
-//               stage (one token, 8 of 64 experts, 2048 x 4096: 15.1 us with
-//               the MMA thread issuing them)
-// The kernel is persistent over items (expert, 128 features, 128 rows); an
-// expert's row blocks of one weight tile are neighbours, so the weight's
-// second read is served by L2.  Two accumulator stages let an item's loads and
-// MMAs run under the epilogue of the one before.
-//
-// With fewer items than SMs, K is split over a cluster of 2, 4 or 8 CTAs.
-// Each leaves its partial sums in its staging buffer and adds a share of the
-// rows from all of them over distributed shared memory, in rank order: no
-// atomics, no workspace, the same bits from run to run.  INT8 partials are
-// added as integers.
+//   warps 2-5   epilogue, one per TMEM lane quarter
+//   warps 6-    (block-scaled formats) a thread per scale atom of a stage, which
+//               copies it to TMEM: a tcgen05.cp holds up the thread that issues
+//               it, and NVFP4 has eight a stage (one token, 8 of 64 experts,
+//               2048 x 4096: 15.1 us with the MMA thread issuing them, 12.7 with
+//               a thread for each)
+// Every wait is bounded; one that runs out latches the error word, the CTA
+// lets what is in flight land and exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -43,17 +39,7 @@
 namespace mxq {
 namespace {
 
-constexpr int GN_STAGES = 5;
-constexpr int GN_W = 128 * 128;        // 128 weight rows x 128 bytes of K
-constexpr int GN_X = 128 * 128;        // up to 128 rows of X
-constexpr int GN_SF = 2048;            // up to 4 scale atoms of 512 bytes, for W and for X
-constexpr int GN_STAGE = GN_W + GN_X + 2 * GN_SF;
-constexpr int GN_STAGING = 32 * 128 * 4;
-constexpr int GN_SMEM = GN_STAGES * GN_STAGE + GN_STAGING + (int)sizeof(Groups) + 256 + 1024;
-constexpr uint32_t GN_TMEM_COLS = 512;
-constexpr uint32_t GN_TMEM_SF = 256;   // two 128-column accumulators, then 32 columns of scales per stage
-static_assert(GN_TMEM_SF + 32 * GN_STAGES <= GN_TMEM_COLS, "TMEM budget");
-static_assert(GN_SMEM <= 227 * 1024, "shared memory budget");
+constexpr int GG_W = 128 * 128;   // a stage's weight: 128 rows x 128 bytes of K
 constexpr unsigned int kErrGrouped = 512u;
 
 struct GroupedParams {
@@ -100,12 +86,12 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 }
 
 template <int F>
-__host__ __device__ constexpr int gn_atoms() { return F == kNVFP4 ? 4 : F == kMXFP4 ? 2 : F == kMXFP8 ? 1 : 0; }
+__host__ __device__ constexpr int gg_atoms() { return F == kNVFP4 ? 4 : F == kMXFP4 ? 2 : F == kMXFP8 ? 1 : 0; }
 template <int F>
-__host__ __device__ constexpr int gn_threads() { return 192 + 32 * gn_atoms<F>(); }
+__host__ __device__ constexpr int gg_threads() { return 192 + 32 * gg_atoms<F>(); }
 // K-major operands; M / 16 at bit 24 and N / 8 at bit 17 are or-ed in.
 template <int F>
-__host__ __device__ constexpr uint32_t gn_idesc() {
+__host__ __device__ constexpr uint32_t gg_idesc() {
     return F == kNVFP4       ? (1u << 7) | (1u << 10)                 // E2M1, UE4M3 scales
            : F == kMXFP4     ? (1u << 7) | (1u << 10) | (1u << 23)    // E2M1, UE8M0 scales
            : F == kMXFP8     ? (1u << 23)                             // E4M3, UE8M0 scales
@@ -236,6 +222,13 @@ template <int F>
 __device__ __forceinline__ float scale_of(const GroupedParams &p, int group) {
     return F == kNVFP4 || F == kFP8Tensor ? __fmul_rn(__ldg(p.x_ts), __ldg(p.w_ts + group)) : 1.0f;
 }
+template <int F>
+__device__ __forceinline__ void prefetch_maps(const GroupedParams &p, int warp, int lane) {
+    if (warp == 0 && lane < (gg_atoms<F>() ? 7 : 5)) {
+        const CUtensorMap *m = lane < 4 ? p.x + lane : lane == 4 ? &p.w : lane == 5 ? &p.sfw : &p.sfx;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+    }
+}
 // Whether all 128 epilogue threads say so: they meet at barriers, so they go
 // on together or not at all.
 __device__ __forceinline__ bool all_epilogue(bool ok) {
@@ -247,8 +240,6 @@ __device__ __forceinline__ bool all_epilogue(bool ok) {
         : "memory");
     return all != 0;
 }
-
-// ---- few rows per expert
 
 // An item: a feature tile of an expert times a block of 128 (or, WIDE, 256) of
 // its rows.  An expert's blocks of one feature tile are neighbours.
@@ -278,267 +269,39 @@ __device__ __forceinline__ Item item_at(const Groups &g, int n_groups, int n_til
     return it;
 }
 
-template <int F>
-__global__ void __launch_bounds__(gn_threads<F>(), 1) k_gemm_grouped_few(const __grid_constant__ GroupedParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint32_t *staging = reinterpret_cast<uint32_t *>(smem + GN_STAGES * GN_STAGE);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + GN_STAGES * GN_STAGE + GN_STAGING);
-    uint64_t *empty = full + GN_STAGES;
-    uint64_t *accf = empty + GN_STAGES;   // [2] accumulator stage full
-    uint64_t *acce = accf + 2;            // [2] accumulator stage drained
-    uint64_t *ready = acce + 2;           // partial sums of every CTA of the cluster in its staging
-    uint64_t *freed = ready + 1;          // and read by all of them
-    uint64_t *drain = freed + 1;
-    uint64_t *sfready = drain + 1;        // [GN_STAGES] a stage's scales in TMEM
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sfready + GN_STAGES);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    Groups &groups = *reinterpret_cast<Groups *>(smem + GN_STAGES * GN_STAGE + GN_STAGING + 256);
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t split;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
-    const uint32_t rank = cluster_rank();
-    const int cid = (int)cluster_id(), ncl = (int)cluster_count();
-    constexpr int NSF = gn_atoms<F>();
-
-    if (warp == 0 && lane < 7) {
-        const CUtensorMap *m = lane < 4 ? p.x + lane : lane == 4 ? &p.w : lane == 5 ? &p.sfw : &p.sfx;
-        if (lane < 5 || NSF) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
-    }
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < GN_STAGES; s++) {
-            mbar_init(full + s, 1);
-            mbar_init(empty + s, 1);
-            mbar_init(sfready + s, NSF ? NSF : 1);
-        }
-        for (int i = 0; i < 2; i++) {
-            mbar_init(accf + i, 1);
-            mbar_init(acce + i, 4);
-        }
-        mbar_init(ready, 4 * split);
-        mbar_init(freed, 4 * split);
-        mbar_init(drain, 1 + NSF);
-        *abort_flag = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(GN_TMEM_COLS));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    tc_fence_before();
-    if (split > 1) cluster_sync();
-    else __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    pdl_wait();
-    pdl_launch_dependents();
-    load_groups(groups, p.offsets, p.n_groups, p.rows, blockIdx.x == 0 ? p.err : nullptr);
-
-    const int tiles = groups.tile[p.n_groups];   // above max_tiles only for offsets out of order
-    const int items = (tiles < p.max_tiles ? tiles : p.max_tiles) * p.n_tiles;
-    const int kt0 = (int)((int64_t)p.num_k_tiles * rank / split), kt1 = (int)((int64_t)p.num_k_tiles * (rank + 1) / split);
-
-    if (warp == 0) {
-        if (lane == 0) {
-            int it = 0;
-            for (int item = cid; item < items && !*abort_flag; item += ncl) {
-                const Item w = item_at<false>(groups, p.n_groups, p.n_tiles, item);
-                const int box = box_of(w.n_rows);
-                const uint32_t bytes = GN_W + ((16u << box) * 128u) + NSF * 1024u;
-                for (int kt = kt0; kt < kt1; kt++, it++) {
-                    const int s = it % GN_STAGES;
-                    if (!mbar_wait(empty + s, ((it / GN_STAGES) & 1) ^ 1, p.wait_ns)) {
-                        atomicOr(p.err, kErrGrouped);
-                        *abort_flag = 1;
-                    }
-                    if (*abort_flag) break;
-                    uint8_t *sw = smem + s * GN_STAGE;
-                    mbar_arrive_expect_tx(full + s, bytes);
-                    tma_load_2d(&p.w, sw, full + s, kt * 128, w.group * p.n + w.tile_n * 128);
-                    tma_load_2d(&p.x[box], sw + GN_W, full + s, kt * 128, w.row0);
-                    if (NSF) {
-                        tma_load_2d(&p.sfw, sw + GN_W + GN_X, full + s, 0, (w.group * p.w_tiles + w.tile_n) * p.s4 + kt * NSF);
-                        tma_load_2d(&p.sfx, sw + GN_W + GN_X + GN_SF, full + s, 0, w.sf_tile * p.s4 + kt * NSF);
-                    }
-                }
-            }
-            if (*abort_flag)   // wait (bounded) for the loads that may still be in flight
-                for (int i = (it > GN_STAGES ? it - GN_STAGES : 0); i < it; i++)
-                    mbar_wait(full + (i % GN_STAGES), (i / GN_STAGES) & 1, p.wait_ns);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            int it = 0, count = 0;
-            const uint64_t ad0 = sdesc_sw128(smem), bd0 = sdesc_sw128(smem + GN_W);
-            for (int item = cid; item < items && !*abort_flag; item += ncl, count++) {
-                const Item w = item_at<false>(groups, p.n_groups, p.n_tiles, item);
-                const uint32_t idesc = gn_idesc<F>() | (8u << 24) | ((uint32_t)((w.n_rows + 15) >> 4) << 18);
-                const int st = count & 1;
-                const uint32_t acc = tmem + 128u * st;
-                bool ok = mbar_wait_spin(acce + st, ((count >> 1) & 1) ^ 1, p.wait_ns);
-                tc_fence_after();
-                for (int kt = kt0; kt < kt1 && ok && !*abort_flag; kt++, it++) {
-                    const int s = it % GN_STAGES;
-                    ok = mbar_wait_spin(NSF ? sfready + s : full + s, (it / GN_STAGES) & 1, p.wait_ns);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t sft = tmem + GN_TMEM_SF + 32u * s;
-                    const int left = (p.kbytes - kt * 128) >> 5, nks = left < 4 ? left : 4;
-                    const uint64_t off = (uint64_t)(s * (GN_STAGE >> 4));
-#pragma unroll
-                    for (int ks = 0; ks < 4; ks++)
-                        if (ks < nks)
-                            mma_step<F, 1>(acc, ad0 + off + 2 * ks, bd0 + off + 2 * ks, idesc, kt > kt0 || ks > 0, sft, 8, ks);
-                    tc_commit(empty + s);
-                }
-                if (!ok) {
-                    atomicOr(p.err, kErrGrouped);
-                    *abort_flag = 1;
-                }
-                if (*abort_flag) break;
-                tc_commit(accf + st);
-            }
-            if (*abort_flag) {   // what is in flight lands before the TMEM is freed
-                tc_commit(drain);
-                mbar_wait(drain, 0, p.wait_ns);
-            }
-        }
-    } else if (warp >= 6) {
-        const int atom = warp - 6;
-        if (lane == 0) {
-            int it = 0;
-            for (int item = cid; item < items && !*abort_flag; item += ncl) {
-                for (int kt = kt0; kt < kt1; kt++, it++) {
-                    const int s = it % GN_STAGES;
-                    if (!mbar_wait(full + s, (it / GN_STAGES) & 1, p.wait_ns)) {
-                        atomicOr(p.err, kErrGrouped);
-                        *abort_flag = 1;
-                    }
-                    if (*abort_flag) break;
-                    tc_fence_after();
-                    // atoms of 32-byte k-steps: 4 (NVFP4: one each), 2 or 1 a stage, fewer in the last
-                    if (atom * (4 / (NSF ? NSF : 1)) * 32 < p.kbytes - kt * 128) {
-                        const uint8_t *sf = smem + s * GN_STAGE + GN_W + GN_X + 512 * atom;
-                        const uint32_t to = tmem + GN_TMEM_SF + 32u * s + 8u * atom;
-                        tc_cp(to, sdesc_atom(sf));
-                        tc_cp(to + 4, sdesc_atom(sf + GN_SF));
-                    }
-                    tc_commit(sfready + s);
-                }
-            }
-            if (*abort_flag) {
-                tc_commit(drain);
-                mbar_wait(drain, 0, p.wait_ns);
-            }
-        }
-    } else {
-        const int q = warp & 3, feature = q * 32 + lane;   // TMEM lane quarter and lane
-        const int et = threadIdx.x - 64;                   // 0 .. 127 among the epilogue threads
-        int count = 0;
-        uint32_t chunks = 0;   // staging rounds done
-        bool ok = true;
-        for (int item = cid; item < items; item += ncl, count++) {
-            const Item w = item_at<false>(groups, p.n_groups, p.n_tiles, item);
-            const int st = count & 1;
-            ok = ok && !*abort_flag && mbar_wait(accf + st, (count >> 1) & 1, p.wait_ns);
-            if (!all_epilogue(ok)) {
-                if (!ok && !*abort_flag) atomicOr(p.err, kErrGrouped);
-                *abort_flag = 1;
-                break;
-            }
-            tc_fence_after();
-            const float alpha = scale_of<F>(p, w.group);
-            const int n0 = w.tile_n * 128, n_chunks = (w.n_rows + 31) >> 5;
-            const float ws =
-                F == kINT8Row && n0 + feature < p.n ? __ldg(p.w_row_scale + (int64_t)w.group * p.n + n0 + feature) : 0.0f;
-            for (int c = 0; c < n_chunks; c++, chunks++) {
-                uint32_t r[32];
-                __syncwarp();
-                tmem_ld_32x32b_x32(tmem + ((uint32_t)(q * 32) << 16) + 128u * st + 32u * c, r);
-                if (c == n_chunks - 1) {   // the accumulator stage is drained
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_local_relaxed(acce + st);
-                }
-                if (split == 1) {
-                    store_chunk<F>(p, r, w.row0 + c * 32, w.n_rows - c * 32, n0 + feature, alpha, ws, lane);
-                    continue;
-                }
-                // the staging of the round before has been read by the cluster
-                if (chunks > 0 && ok) ok = mbar_wait<true>(freed, (chunks - 1) & 1, p.wait_ns);
-#pragma unroll
-                for (int j = 0; j < 32; j++) staging[j * 128 + feature] = r[j];
-                __syncwarp();
-                if (lane < (int)split) mbar_arrive_remote(map_to_rank(ready, lane));
-                if (ok) ok = mbar_wait<true>(ready, chunks & 1, p.wait_ns);
-                // rows rank * 32 / split .. of the chunk, 8 features per thread
-                const int per = 32 / (int)split, v8 = et & 15;
-                for (int j = et >> 4; j < per && ok; j += 8) {
-                    const int jr = (int)rank * per + j, row = w.row0 + c * 32 + jr;
-                    if (c * 32 + jr >= w.n_rows) break;
-                    const uint32_t *src = staging + jr * 128 + v8 * 8;
-                    float v[8] = {};
-                    int vi[8] = {};
-                    for (uint32_t s = 0; s < split; s++) {
-                        const uint32_t at = map_to_rank(src, s);
-                        const float4 a = ld_cluster_f4(at), b = ld_cluster_f4(at + 16);
-                        const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            if (F == kINT8Row) vi[i] += __float_as_int(u[i]);
-                            else v[i] = __fadd_rn(v[i], u[i]);
-                        }
-                    }
-                    if (F == kINT8Row) {
-#pragma unroll
-                        for (int i = 0; i < 8; i++) v[i] = (float)vi[i];
-                    }
-                    store_row8<F>(p, v, w.group, row, n0 + v8 * 8, alpha);
-                }
-                __syncwarp();
-                if (lane < (int)split) mbar_arrive_remote(map_to_rank(freed, lane));
-            }
-            if (!ok) {
-                if (!*abort_flag) atomicOr(p.err, kErrGrouped);
-                *abort_flag = 1;
-            }
-        }
-    }
-
-    tc_fence_before();
-    if (split > 1) cluster_sync();   // no CTA leaves while another may read its staging
-    else __syncthreads();
-    if (warp == 1) {
-        __syncwarp();
-        tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(GN_TMEM_COLS));
-    }
-}
-
-// ---- many rows per expert
+// ---- pairs
 //
-// A pair of CTAs (cta_group::2) computes 256 features x up to 256 rows: each
-// stages its 128 weight rows and half of the block's rows of X, holds the
-// scales of its weight rows and of all rows of X, and its 128 features x N
-// accumulator.  N is the block's rows rounded up to 32, so a ragged block costs
-// what it has, in MMA time and in loads.  Warps as in the few-rows kernel; the
-// first CTA's MMA and scale threads serve both.  The accumulator stages lie at
-// columns 0 and GP_ACC1 and share columns with a full block (two of 256 do not
-// fit beside the scales): the epilogue takes the shared chunks to registers
-// first and releases them.
-
-constexpr int GP_STAGES = 5;
-constexpr int GP_SF = 6144;   // W's atoms at 0, X's first 128 rows' at 2048, the others' at 4096
-constexpr int GP_STAGE = GN_W + GN_X + GP_SF;
-constexpr int GP_SMEM = GP_STAGES * GP_STAGE + (int)sizeof(Groups) + 256 + 1024;
-static_assert(GP_SMEM <= 227 * 1024, "shared memory budget");
-constexpr uint32_t GP_SF_PITCH = 12, GP_SF_COLS = 48, GP_SF_GROUPS = 2;   // per atom, per stage; stages in TMEM at a time
-template <int F>
-__host__ __device__ constexpr uint32_t gp_acc1() { return gn_atoms<F>() ? 160u : 256u; }
-constexpr uint32_t GP_TMEM_SF = 512 - GP_SF_GROUPS * GP_SF_COLS;
-static_assert(160 + 256 <= GP_TMEM_SF, "TMEM budget");
+// A pair of CTAs (cta_group::2) computes 256 features x a block of up to NB
+// rows: each stages its 128 weight rows and half of the block's rows of X,
+// holds the scales of its weight rows and of all rows of X, and its 128
+// features x N accumulator.  N is the block's rows rounded up to 32, so a
+// ragged block costs what it has.  The first CTA's MMA and scale threads serve
+// both.  An expert's blocks of one feature tile are neighbours among the items,
+// so the weight's second read is served by L2; two accumulator stages let an
+// item's loads and MMAs run under the epilogue of the one before.
+//   NB = 128: two accumulators of 128 columns leave every stage of the ring
+//     its own scale columns, so the copies run as far ahead as the loads.
+//   NB = 256: the accumulator stages lie at columns 0 and 160 and share columns
+//     with a full block (two of 256 do not fit beside the scales): the epilogue
+//     takes the shared chunks to registers first and releases them; two stages'
+//     scales in TMEM at a time.
+template <int F, int NB>
+struct Pair {
+    static constexpr int kAtoms = gg_atoms<F>();
+    static constexpr int kXBytes = NB / 2 * 128;
+    static constexpr int kSfBytes = 2048 + NB * 16;        // W's atoms, then X's by 128 rows
+    static constexpr int kStage = GG_W + kXBytes + kSfBytes;
+    static constexpr int kStages = NB == 128 ? 7 : 5;
+    static constexpr int kSmem = kStages * kStage + (int)sizeof(Groups) + 256 + 1024;
+    static constexpr uint32_t kPitch = 4 + NB / 32;        // scale columns per atom
+    static constexpr uint32_t kSfCols = 4 * kPitch;        // per stage
+    static constexpr uint32_t kSfGroups = NB == 128 ? kStages : 2;   // stages whose scales TMEM holds
+    static constexpr uint32_t kTmemSf = 512 - kSfGroups * kSfCols;
+    static constexpr uint32_t kAcc1 = NB == 128 ? 128 : kAtoms ? 160 : 256;
+    static constexpr int kShared = NB == 256 && kAtoms ? 3 : 0;      // 32-column chunks that both accumulators use
+    static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024, "shared memory budget");
+    static_assert(kAcc1 + NB <= (kAtoms ? kTmemSf : 512u) && kAcc1 + 32 * kShared >= (uint32_t)NB, "TMEM budget");
+};
 
 __device__ __forceinline__ void tma_load_pair(const CUtensorMap *map, void *dst, uint32_t bar, int c0, int c1) {
     asm volatile(
@@ -563,33 +326,33 @@ __device__ __forceinline__ void tc_cp_pair(uint32_t taddr, uint64_t sdesc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
-template <int F>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gn_threads<F>(), 1)
-    k_gemm_grouped_many(const __grid_constant__ GroupedParams p) {
+template <int F, int NB>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gg_threads<F>(), 1)
+    k_gemm_grouped_pair(const __grid_constant__ GroupedParams p) {
+    using P = Pair<F, NB>;
+    constexpr int ST = P::kStages;
+    constexpr bool WIDE = NB == 256;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + GP_STAGES * GP_STAGE);   // (used in the first CTA)
-    uint64_t *empty = full + GP_STAGES;
-    uint64_t *accf = empty + GP_STAGES;      // [2] accumulator stage full
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + ST * P::kStage);   // (used in the first CTA)
+    uint64_t *empty = full + ST;
+    uint64_t *accf = empty + ST;      // [2] accumulator stage full
     uint64_t *acce = accf + 2;               // [2] drained (first CTA)
     uint64_t *ovlf = acce + 2;               // shared columns drained (first CTA)
     uint64_t *drain = ovlf + 1;
-    uint64_t *sfready = drain + 1;           // [GP_STAGES] a stage's scales in TMEM (first CTA)
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sfready + GP_STAGES);
+    uint64_t *sfready = drain + 1;           // [ST] a stage's scales in TMEM (first CTA)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sfready + ST);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    Groups &groups = *reinterpret_cast<Groups *>(smem + GP_STAGES * GP_STAGE + 256);
+    Groups &groups = *reinterpret_cast<Groups *>(smem + ST * P::kStage + 256);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int cid = (int)cluster_id(), ncl = (int)cluster_count();
-    constexpr int NSF = gn_atoms<F>();
+    constexpr int NSF = gg_atoms<F>();
 
-    if (warp == 0 && lane < 7) {
-        const CUtensorMap *m = lane < 4 ? p.x + lane : lane == 4 ? &p.w : lane == 5 ? &p.sfw : &p.sfx;
-        if (lane < 5 || NSF) asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
-    }
+    prefetch_maps<F>(p, warp, lane);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < GP_STAGES; s++) {
+        for (int s = 0; s < ST; s++) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
             mbar_init(sfready + s, NSF ? NSF : 1);
@@ -605,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gn_threads<F>(), 1)
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(GN_TMEM_COLS));
+                     "r"(512u));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     tc_fence_before();
@@ -615,32 +378,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gn_threads<F>(), 1)
     pdl_wait();
     pdl_launch_dependents();
     load_groups(groups, p.offsets, p.n_groups, p.rows, blockIdx.x == 0 ? p.err : nullptr);
-    const int blocks = groups.wide[p.n_groups];   // above max_tiles only for offsets out of order
+    const int blocks = (WIDE ? groups.wide : groups.tile)[p.n_groups];   // above max_tiles only for offsets out of order
     const int items = (blocks < p.max_tiles ? blocks : p.max_tiles) * p.n_tiles;
 
     if (warp == 0) {
         if (lane == 0) {
             int it = 0;
             for (int item = cid; item < items && !*abort_flag; item += ncl) {
-                const Item w = item_at<true>(groups, p.n_groups, p.n_tiles, item);
+                const Item w = item_at<WIDE>(groups, p.n_groups, p.n_tiles, item);
                 const int half = ((w.n_rows + 31) >> 5) << 4;   // rows of X in each CTA
                 const int box = box_of(half);
-                const bool hi = w.n_rows > 128;                 // X's second scale tile
-                const uint32_t bytes = 2u * (GN_W + (2048u << box)) + NSF * 512u * 2u * (hi ? 3u : 2u);
+                const bool hi = WIDE && w.n_rows > 128;         // X's second scale tile
+                const uint32_t bytes = 2u * (GG_W + (2048u << box)) + NSF * 512u * 2u * (hi ? 3u : 2u);
                 const int wrow = w.group * p.n + w.tile_n * 256 + (int)rank * 128, xrow = w.row0 + (int)rank * half;
                 const int wsf = w.group * p.w_tiles + w.tile_n * 2 + (int)rank;
                 for (int kt = 0; kt < p.num_k_tiles; kt++, it++) {
-                    const int s = it % GP_STAGES;
-                    if (!mbar_wait(empty + s, ((it / GP_STAGES) & 1) ^ 1, p.wait_ns)) {
+                    const int s = it % ST;
+                    if (!mbar_wait(empty + s, ((it / ST) & 1) ^ 1, p.wait_ns)) {
                         atomicOr(p.err, kErrGrouped);
                         *abort_flag = 1;
                     }
                     if (*abort_flag) break;
-                    uint8_t *sw = smem + s * GP_STAGE, *sf = sw + GN_W + GN_X;
+                    uint8_t *sw = smem + s * P::kStage, *sf = sw + GG_W + P::kXBytes;
                     const uint32_t bar = map_to_rank(full + s, 0);
                     if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
                     tma_load_pair(&p.w, sw, bar, kt * 128, wrow);
-                    tma_load_pair(&p.x[box], sw + GN_W, bar, kt * 128, xrow);
+                    tma_load_pair(&p.x[box], sw + GG_W, bar, kt * 128, xrow);
                     if (NSF) {
                         tma_load_pair(&p.sfw, sf, bar, 0, wsf * p.s4 + kt * NSF);
                         tma_load_pair(&p.sfx, sf + 2048, bar, 0, w.sf_tile * p.s4 + kt * NSF);
@@ -649,36 +412,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gn_threads<F>(), 1)
                 }
             }
             if (*abort_flag && rank == 0)   // wait (bounded) for the loads that may still be in flight
-                for (int i = (it > GP_STAGES ? it - GP_STAGES : 0); i < it; i++)
-                    mbar_wait(full + (i % GP_STAGES), (i / GP_STAGES) & 1, p.wait_ns);
+                for (int i = (it > ST ? it - ST : 0); i < it; i++)
+                    mbar_wait(full + (i % ST), (i / ST) & 1, p.wait_ns);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             int it = 0, count = 0, s = 0;
             uint32_t ph = 0;
-            const uint64_t ad0 = sdesc_sw128(smem), bd0 = sdesc_sw128(smem + GN_W);
+            const uint64_t ad0 = sdesc_sw128(smem), bd0 = sdesc_sw128(smem + GG_W);
             for (int item = cid; item < items && !*abort_flag; item += ncl, count++) {
-                const Item w = item_at<true>(groups, p.n_groups, p.n_tiles, item);
-                const uint32_t idesc = gn_idesc<F>() | (16u << 24) | ((uint32_t)((w.n_rows + 31) >> 5) << 19);
+                const Item w = item_at<WIDE>(groups, p.n_groups, p.n_tiles, item);
+                const uint32_t idesc = gg_idesc<F>() | (16u << 24) | ((uint32_t)((w.n_rows + 31) >> 5) << 19);
                 const int st = count & 1;
-                const uint32_t acc = tmem + (st ? gp_acc1<F>() : 0u);
+                const uint32_t acc = tmem + (st ? P::kAcc1 : 0u);
                 // this stage drained (item count - 2) and the shared columns (item count - 1), in both CTAs
                 bool ok = mbar_wait_spin<true>(acce + st, ((count >> 1) & 1) ^ 1, p.wait_ns);
-                if (NSF && ok && count > 0) ok = mbar_wait_spin<true>(ovlf, (count - 1) & 1, p.wait_ns);
+                if (P::kShared && ok && count > 0) ok = mbar_wait_spin<true>(ovlf, (count - 1) & 1, p.wait_ns);
                 tc_fence_after();
                 for (int kt = 0; kt < p.num_k_tiles && ok && !*abort_flag; kt++, it++) {
                     ok = mbar_wait_spin(NSF ? sfready + s : full + s, ph, p.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sft = tmem + GP_TMEM_SF + GP_SF_COLS * ((uint32_t)it % GP_SF_GROUPS);
+                    const uint32_t sft = tmem + P::kTmemSf + P::kSfCols * ((uint32_t)it % P::kSfGroups);
                     const int left = (p.kbytes - kt * 128) >> 5;
-                    const uint64_t off = (uint64_t)(s * (GP_STAGE >> 4));
+                    const uint64_t off = (uint64_t)(s * (P::kStage >> 4));
 #pragma unroll
                     for (int ks = 0; ks < 4; ks++)
                         if (ks < left)
-                            mma_step<F, 2>(acc, ad0 + off + 2 * ks, bd0 + off + 2 * ks, idesc, (kt | ks) != 0, sft, GP_SF_PITCH, ks);
+                            mma_step<F, 2>(acc, ad0 + off + 2 * ks, bd0 + off + 2 * ks, idesc, (kt | ks) != 0, sft, P::kPitch, ks);
                     tc_commit_pair(empty + s);
-                    if (++s == GP_STAGES) {
+                    if (++s == ST) {
                         s = 0;
                         ph ^= 1u;
                     }
@@ -700,13 +463,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gn_threads<F>(), 1)
         if (NSF && lane == 0 && rank == 0) {
             int it = 0;
             for (int item = cid; item < items && !*abort_flag; item += ncl) {
-                const bool hi = item_at<true>(groups, p.n_groups, p.n_tiles, item).n_rows > 128;
+                const bool hi = WIDE && item_at<WIDE>(groups, p.n_groups, p.n_tiles, item).n_rows > 128;
                 for (int kt = 0; kt < p.num_k_tiles; kt++, it++) {
-                    const int s = it % GP_STAGES;
-                    bool ok = mbar_wait(full + s, (it / GP_STAGES) & 1, p.wait_ns);
-                    // these columns were last read by the MMAs of k-tile it - GP_SF_GROUPS
-                    const int prev = it - (int)GP_SF_GROUPS;
-                    if (ok && prev >= 0) ok = mbar_wait(empty + prev % GP_STAGES, (prev / GP_STAGES) & 1, p.wait_ns);
+                    const int s = it % ST;
+                    bool ok = mbar_wait(full + s, (it / ST) & 1, p.wait_ns);
+                    // these columns were last read by the MMAs of k-tile it - kSfGroups (a stage of its own: when it was loaded)
+                    const int prev = it - (int)P::kSfGroups;
+                    if ((int)P::kSfGroups < ST && ok && prev >= 0) ok = mbar_wait(empty + prev % ST, (prev / ST) & 1, p.wait_ns);
                     if (!ok) {
                         atomicOr(p.err, kErrGrouped);
                         *abort_flag = 1;
@@ -714,8 +477,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gn_threads<F>(), 1)
                     if (*abort_flag) break;
                     tc_fence_after();
                     if (atom * (4 / (NSF ? NSF : 1)) * 32 < p.kbytes - kt * 128) {
-                        const uint8_t *sf = smem + s * GP_STAGE + GN_W + GN_X + 512 * atom;
-                        const uint32_t to = tmem + GP_TMEM_SF + GP_SF_COLS * ((uint32_t)it % GP_SF_GROUPS) + GP_SF_PITCH * atom;
+                        const uint8_t *sf = smem + s * P::kStage + GG_W + P::kXBytes + 512 * atom;
+                        const uint32_t to = tmem + P::kTmemSf + P::kSfCols * ((uint32_t)it % P::kSfGroups) + P::kPitch * atom;
                         tc_cp_pair(to, sdesc_atom(sf));
                         tc_cp_pair(to + 4, sdesc_atom(sf + 2048));
                         if (hi) tc_cp_pair(to + 8, sdesc_atom(sf + 4096));
@@ -733,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gn_threads<F>(), 1)
         const uint32_t ovl_to = map_to_rank(ovlf, 0), acce_to = map_to_rank(acce, 0);   // acce + 1: 8 bytes on
         int count = 0;
         for (int item = cid; item < items; item += ncl, count++) {
-            const Item w = item_at<true>(groups, p.n_groups, p.n_tiles, item);
+            const Item w = item_at<WIDE>(groups, p.n_groups, p.n_tiles, item);
             const int st = count & 1;
             const bool ok = !*abort_flag && mbar_wait(accf + st, (count >> 1) & 1, p.wait_ns);
             if (!all_epilogue(ok)) {
@@ -743,14 +506,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gn_threads<F>(), 1)
             }
             tc_fence_after();
             const float alpha = scale_of<F>(p, w.group);
-            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (st ? gp_acc1<F>() : 0u);
+            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + (st ? P::kAcc1 : 0u);
             const int col = w.tile_n * 256 + (int)rank * 128 + feature, n_chunks = (w.n_rows + 31) >> 5;
             const float ws = F == kINT8Row && col < p.n ? __ldg(p.w_row_scale + (int64_t)w.group * p.n + col) : 0.0f;
             auto process = [&](int c, const uint32_t (&r)[32]) {   // 32 rows of the block
                 store_chunk<F>(p, r, w.row0 + c * 32, w.n_rows - c * 32, col, alpha, ws, lane);
             };
             // chunks [first, first + shared) lie in columns that the other stage uses too
-            constexpr int kShared = NSF ? 3 : 0;   // columns 160 .. 255
+            constexpr int kShared = P::kShared;
             int first = 0, shared = 0;
             if constexpr (kShared > 0) {
                 first = st ? 0 : 5;
@@ -796,23 +559,230 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gn_threads<F>(), 1)
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(GN_TMEM_COLS));
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+    }
+}
+
+// ---- K split over a cluster
+//
+// A cluster holds one item, 128 features x up to 128 rows; CTA r of S does
+// k-tiles [KT r / S, KT (r + 1) / S) with cta_group::1 MMAs, leaves its sums by
+// chunks of 32 rows in shared memory, and adds its share of a chunk's rows from
+// all CTAs over distributed shared memory in rank order: no atomics, no
+// workspace, the same bits from run to run.  INT8 sums are added as integers.
+
+constexpr int GS_STAGES = 5;
+constexpr int GS_X = 128 * 128;
+constexpr int GS_SF = 2048;   // up to 4 atoms, for W and for X
+constexpr int GS_STAGE = GG_W + GS_X + 2 * GS_SF;
+constexpr int GS_STAGING = 32 * 128 * 4;
+constexpr int GS_SMEM = GS_STAGES * GS_STAGE + GS_STAGING + (int)sizeof(Groups) + 256 + 1024;
+constexpr uint32_t GS_TMEM_SF = 128;   // the accumulator's 128 columns, then 32 of scales per stage
+static_assert(GS_TMEM_SF + 32 * GS_STAGES <= 512, "TMEM budget");
+static_assert(GS_SMEM <= 227 * 1024, "shared memory budget");
+
+template <int F>
+__global__ void __launch_bounds__(gg_threads<F>(), 1) k_gemm_grouped_split(const __grid_constant__ GroupedParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint32_t *staging = reinterpret_cast<uint32_t *>(smem + GS_STAGES * GS_STAGE);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + GS_STAGES * GS_STAGE + GS_STAGING);
+    uint64_t *empty = full + GS_STAGES;
+    uint64_t *sfready = empty + GS_STAGES;   // [GS_STAGES] a stage's scales in TMEM
+    uint64_t *accf = sfready + GS_STAGES;    // the sums are in TMEM
+    uint64_t *ready = accf + 1;              // a chunk of every CTA's sums is in its staging
+    uint64_t *freed = ready + 1;             // and has been read by all of them
+    uint64_t *drain = freed + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    Groups &groups = *reinterpret_cast<Groups *>(smem + GS_STAGES * GS_STAGE + GS_STAGING + 256);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t split;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+    const uint32_t rank = cluster_rank();
+    const int item = (int)cluster_id();
+    constexpr int NSF = gg_atoms<F>();
+
+    prefetch_maps<F>(p, warp, lane);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < GS_STAGES; s++) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+            mbar_init(sfready + s, NSF ? NSF : 1);
+        }
+        mbar_init(accf, 1);
+        mbar_init(ready, 4 * split);
+        mbar_init(freed, 4 * split);
+        mbar_init(drain, 1 + NSF);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+    load_groups(groups, p.offsets, p.n_groups, p.rows, blockIdx.x == 0 ? p.err : nullptr);
+    const int blocks = groups.tile[p.n_groups];   // above max_tiles only for offsets out of order
+    const bool work = item < (blocks < p.max_tiles ? blocks : p.max_tiles) * p.n_tiles;   // (the grid has the most items there can be)
+
+    if (work) {
+        const Item w = item_at<false>(groups, p.n_groups, p.n_tiles, item);
+        const int kt0 = (int)((int64_t)p.num_k_tiles * rank / split), n_kt = (int)((int64_t)p.num_k_tiles * (rank + 1) / split) - kt0;
+        if (warp == 0) {
+            if (lane == 0) {
+                const int box = box_of(w.n_rows);
+                const uint32_t bytes = GG_W + (2048u << box) + NSF * 1024u;
+                int it = 0;
+                for (; it < n_kt; it++) {
+                    const int s = it % GS_STAGES, kt = kt0 + it;
+                    if (!mbar_wait(empty + s, ((it / GS_STAGES) & 1) ^ 1, p.wait_ns)) {
+                        atomicOr(p.err, kErrGrouped);
+                        *abort_flag = 1;
+                    }
+                    if (*abort_flag) break;
+                    uint8_t *sw = smem + s * GS_STAGE, *sf = sw + GG_W + GS_X;
+                    mbar_arrive_expect_tx(full + s, bytes);
+                    tma_load_2d(&p.w, sw, full + s, kt * 128, w.group * p.n + w.tile_n * 128);
+                    tma_load_2d(&p.x[box], sw + GG_W, full + s, kt * 128, w.row0);
+                    if (NSF) {
+                        tma_load_2d(&p.sfw, sf, full + s, 0, (w.group * p.w_tiles + w.tile_n) * p.s4 + kt * NSF);
+                        tma_load_2d(&p.sfx, sf + GS_SF, full + s, 0, w.sf_tile * p.s4 + kt * NSF);
+                    }
+                }
+                if (*abort_flag)   // wait (bounded) for the loads that may still be in flight
+                    for (int i = (it > GS_STAGES ? it - GS_STAGES : 0); i < it; i++)
+                        mbar_wait(full + (i % GS_STAGES), (i / GS_STAGES) & 1, p.wait_ns);
+            }
+        } else if (warp == 1) {
+            if (lane == 0) {
+                const uint64_t ad0 = sdesc_sw128(smem), bd0 = sdesc_sw128(smem + GG_W);
+                const uint32_t idesc = gg_idesc<F>() | (8u << 24) | ((uint32_t)((w.n_rows + 15) >> 4) << 18);
+                for (int it = 0; it < n_kt; it++) {
+                    const int s = it % GS_STAGES;
+                    if (!mbar_wait_spin(NSF ? sfready + s : full + s, (it / GS_STAGES) & 1, p.wait_ns)) {
+                        atomicOr(p.err, kErrGrouped);
+                        *abort_flag = 1;
+                    }
+                    if (*abort_flag) break;
+                    tc_fence_after();
+                    const int left = (p.kbytes - (kt0 + it) * 128) >> 5;
+                    const uint64_t off = (uint64_t)(s * (GS_STAGE >> 4));
+#pragma unroll
+                    for (int ks = 0; ks < 4; ks++)
+                        if (ks < left)
+                            mma_step<F, 1>(tmem, ad0 + off + 2 * ks, bd0 + off + 2 * ks, idesc, (it | ks) != 0,
+                                           tmem + GS_TMEM_SF + 32u * s, 8, ks);
+                    tc_commit(empty + s);
+                }
+                if (!*abort_flag) {
+                    tc_commit(accf);
+                } else {   // what is in flight lands before the TMEM is freed
+                    tc_commit(drain);
+                    mbar_wait(drain, 0, p.wait_ns);
+                }
+            }
+        } else if (warp >= 6) {
+            const int atom = warp - 6;
+            if (lane == 0) {
+                for (int it = 0; it < n_kt; it++) {
+                    const int s = it % GS_STAGES;
+                    if (!mbar_wait(full + s, (it / GS_STAGES) & 1, p.wait_ns)) {
+                        atomicOr(p.err, kErrGrouped);
+                        *abort_flag = 1;
+                    }
+                    if (*abort_flag) break;
+                    tc_fence_after();
+                    if (atom * (4 / (NSF ? NSF : 1)) * 32 < p.kbytes - (kt0 + it) * 128) {
+                        const uint8_t *sf = smem + s * GS_STAGE + GG_W + GS_X + 512 * atom;
+                        const uint32_t to = tmem + GS_TMEM_SF + 32u * s + 8u * atom;
+                        tc_cp(to, sdesc_atom(sf));
+                        tc_cp(to + 4, sdesc_atom(sf + GS_SF));
+                    }
+                    tc_commit(sfready + s);
+                }
+                if (*abort_flag) {
+                    tc_commit(drain);
+                    mbar_wait(drain, 0, p.wait_ns);
+                }
+            }
+        } else {
+            const int q = warp & 3, feature = q * 32 + lane;   // TMEM lane quarter and lane
+            const int et = threadIdx.x - 64, v8 = et & 15;     // 0 .. 127 among the epilogue threads; 8 features to store
+            const int per = 32 / (int)split, n_chunks = (w.n_rows + 31) >> 5;
+            const float alpha = scale_of<F>(p, w.group);
+            bool ok = mbar_wait(accf, 0, p.wait_ns) && !*abort_flag;
+            tc_fence_after();
+            for (int c = 0; c < n_chunks; c++) {
+                uint32_t r[32];
+                __syncwarp();
+                tmem_ld_32x32b_x32(tmem + ((uint32_t)(q * 32) << 16) + 32u * c, r);
+                if (c > 0 && ok) ok = mbar_wait<true>(freed, (c - 1) & 1, p.wait_ns);
+#pragma unroll
+                for (int j = 0; j < 32; j++) staging[j * 128 + feature] = r[j];
+                __syncwarp();
+                if (lane < (int)split) mbar_arrive_remote(map_to_rank(ready, lane));
+                if (ok) ok = mbar_wait<true>(ready, c & 1, p.wait_ns);
+                // rows rank * per .. of the chunk, 8 features per thread
+                for (int j = et >> 4; j < per && ok; j += 8) {
+                    const int jr = (int)rank * per + j;
+                    if (c * 32 + jr >= w.n_rows) break;
+                    float v[8] = {};
+                    int vi[8] = {};
+                    for (uint32_t s = 0; s < split; s++) {
+                        const uint32_t at = map_to_rank(staging + jr * 128 + v8 * 8, s);
+                        const float4 a = ld_cluster_f4(at), b = ld_cluster_f4(at + 16);
+                        const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int i = 0; i < 8; i++) {
+                            if (F == kINT8Row) vi[i] += __float_as_int(u[i]);
+                            else v[i] = __fadd_rn(v[i], u[i]);
+                        }
+                    }
+                    if (F == kINT8Row) {
+#pragma unroll
+                        for (int i = 0; i < 8; i++) v[i] = (float)vi[i];
+                    }
+                    store_row8<F>(p, v, w.group, w.row0 + c * 32 + jr, w.tile_n * 128 + v8 * 8, alpha);
+                }
+                __syncwarp();
+                if (lane < (int)split) mbar_arrive_remote(map_to_rank(freed, lane));
+            }
+            if (!ok) {
+                if (!*abort_flag) atomicOr(p.err, kErrGrouped);
+                *abort_flag = 1;
+            }
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync();   // no CTA leaves while another may read its staging
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
     }
 }
 
 // ------------------------------------------------------------------ host
 
 template <int F>
-cudaError_t launch_few(const GroupedParams &p, int clusters, int split, cudaStream_t s) {
+cudaError_t launch_split(const GroupedParams &p, int clusters, int split, cudaStream_t s) {
     static PerDeviceOnce smem_opt_in;
     cudaError_t e = smem_opt_in.run([] {
-        return cudaFuncSetAttribute(k_gemm_grouped_few<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, GN_SMEM);
+        return cudaFuncSetAttribute(k_gemm_grouped_split<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, GS_SMEM);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * split), 1, 1);
-    cfg.blockDim = dim3(gn_threads<F>(), 1, 1);
-    cfg.dynamicSmemBytes = GN_SMEM;
+    cfg.blockDim = dim3(gg_threads<F>(), 1, 1);
+    cfg.dynamicSmemBytes = GS_SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[2] = {pdl_attribute()};
     attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -820,46 +790,54 @@ cudaError_t launch_few(const GroupedParams &p, int clusters, int split, cudaStre
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_gemm_grouped_few<F>, p);
+    return cudaLaunchKernelEx(&cfg, k_gemm_grouped_split<F>, p);
 }
 
-template <int F>
-cudaError_t launch_many(const GroupedParams &p, int clusters, cudaStream_t s) {
+template <int F, int NB>
+cudaError_t launch_pair(const GroupedParams &p, int clusters, cudaStream_t s) {
+    constexpr int smem = Pair<F, NB>::kSmem;
     static PerDeviceOnce smem_opt_in;
     cudaError_t e = smem_opt_in.run([] {
-        return cudaFuncSetAttribute(k_gemm_grouped_many<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, GP_SMEM);
+        return cudaFuncSetAttribute(k_gemm_grouped_pair<F, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
-    cfg.blockDim = dim3(gn_threads<F>(), 1, 1);
-    cfg.dynamicSmemBytes = GP_SMEM;
+    cfg.blockDim = dim3(gg_threads<F>(), 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_gemm_grouped_many<F>, p);
+    return cudaLaunchKernelEx(&cfg, k_gemm_grouped_pair<F, NB>, p);
 }
 
-// The host knows the rows of all experts together, not of each: their mean
-// decides between the kernels.
+// The host knows the rows of all experts together, not of each; blocks: what
+// they can need at most.
+//   K is split S ways while the items leave SMs idle (items S 2 <= SMs) and
+//   every CTA keeps two k-tiles, up to 4 (one token, 2 of 8 experts, MXFP8: 2048
+//   x 4096 8.4 against 15.4 us by pairs; 1024 x 2048 11.2 us with clusters of 8,
+//   9.6 by pairs).
+//   Else pairs; blocks of 128 rows up to a mean of 80 rows per expert, of 256
+//   above (8 experts of 4096 x 4096, MXFP8: mean 64 30.8 against 33.9 us, mean
+//   128 42.6 against 36.0).
+constexpr int kMaxSplit = 4;
 template <int F>
 cudaError_t launch_fmt(GroupedParams &p, const GroupedOperands &op, cudaStream_t s) {
     const int sms = sm_count();
     const int64_t ragged = op.rows < op.n_groups ? op.rows : op.n_groups;   // blocks that may be partly filled
-    if (op.rows > 64 * (int64_t)op.n_groups) {
-        p.n_tiles = (int)((op.n + 255) / 256);
-        p.max_tiles = (int)(op.rows / 256 + ragged);
-        const int64_t items = (int64_t)p.max_tiles * p.n_tiles;
-        return launch_many<F>(p, (int)(items < sms / 2 ? items : sms / 2), s);
-    }
     p.n_tiles = p.w_tiles;
     p.max_tiles = (int)(op.rows / 128 + ragged);
-    // K is split while the items at most leave SMs idle and every CTA keeps at least two stages
-    const int64_t items = (int64_t)p.max_tiles * p.n_tiles;
+    int64_t items = (int64_t)p.max_tiles * p.n_tiles;
     int split = 1;
-    while (split < 8 && items * split * 2 <= sms && p.num_k_tiles >= split * 4) split *= 2;
-    return launch_few<F>(p, (int)(items < sms / split ? items : sms / split), split, s);
+    while (split < kMaxSplit && items * split * 2 <= sms && p.num_k_tiles >= split * 4) split *= 2;
+    if (split > 1) return launch_split<F>(p, (int)items, split, s);
+    const bool wide = op.rows > 80 * (int64_t)op.n_groups;
+    p.n_tiles = (int)((op.n + 255) / 256);
+    if (wide) p.max_tiles = (int)(op.rows / 256 + ragged);
+    items = (int64_t)p.max_tiles * p.n_tiles;
+    const int clusters = (int)(items < sms / 2 ? items : sms / 2);
+    return wide ? launch_pair<F, 256>(p, clusters, s) : launch_pair<F, 128>(p, clusters, s);
 }
 
 }  // namespace

@@ -242,8 +242,12 @@ MANY = [([700, 0, 513, 256, 1000], 264, 512), ([600], 100, 320), ([129, 1000, 51
         ([900, 31, 0, 1500], 1160, 64)]
 
 
+# more items than pairs of SMs, so that a pair goes on to a second one: blocks of 128 rows, and of 256
+MIXED = [([100, 5, 64, 128, 33, 1], 2560, 320), ([260, 90, 250, 256, 31, 512], 4608, 256), ([200, 70, 256, 33, 161], 4608, 192)]
+
+
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("counts,n,k", FEW + MANY)
+@pytest.mark.parametrize("counts,n,k", FEW + MANY + MIXED)
 def test_product(mxq, orc, fmt, counts, n, k):
     ex = Experts(mxq, orc, fmt, counts, n, k, extra=5)
     ex.check(mxq, torch.float32)
