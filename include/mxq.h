@@ -637,7 +637,8 @@ mxq_status mxq_qlinear_routed(const void *x, int32_t xdtype, int64_t m, int64_t 
  * A part of the experts: pass offsets + first, n_groups = count and the
  * weight of those experts; slots outside [offsets[first],
  * offsets[first + count]) are passed over.
- * Limits: rows <= 2^22, 1 <= experts <= 512, 1 <= topk <= 32.
+ * Limits: rows <= 2^22, 1 <= experts <= 512, 1 <= topk <= 32, byte scales
+ * below 2^34 bytes.
  * Offsets are device data: ones outside [0, rows] or out of order are
  * clamped, so that no access leaves the buffers, and reported by mxq_check()
  * as MXQ_EINVAL. */
@@ -670,7 +671,7 @@ mxq_status mxq_grouped_scales_bytes(int32_t fmt, int64_t rows, int32_t n_groups,
  *   fmt: MXFP8, MXFP4, NVFP4, INT8_ROW or FP8_TENSOR (INT4: MXQ_EUNSUPPORTED).
  *   hadamard_b: as mxq_quantize.
  *   offsets: device int32[n_groups + 1].
- *   slot: device int32[x_rows][topk], or NULL: x is in expert order already
+ *   slot: device int32[x_rows][topk], no row named twice, or NULL: x is in expert order already
  *     (topk == 1, row t is row t, x_rows <= rows; the second linear of an
  *     expert's MLP).
  *   rows: capacity of codes and scales.

@@ -851,6 +851,11 @@ bool grouped_fmt(int32_t f) {   // formats whose GEMM applies the scales without
 bool valid_groups(int64_t rows, int32_t n_groups) {
     return rows >= 0 && rows <= kMaxGroupedRows && n_groups >= 1 && n_groups <= kMaxGroups;
 }
+// The quantizer counts the grouped scales' 4-byte words in 32 bits.
+bool valid_grouped_scales(int32_t fmt, int64_t rows, int32_t n_groups, int64_t cols) {
+    if (!fmt_byte_scales(fmt)) return true;
+    return grouped_scale_tiles(rows, n_groups) * (round_up(cols / fmt_block(fmt), 16) / 4) < ((int64_t)1 << 25);
+}
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
@@ -880,6 +885,7 @@ mxq_status mxq_expert_plan(const void *expert_ids, int32_t id_bits, int64_t rows
 mxq_status mxq_grouped_scales_bytes(int32_t fmt, int64_t rows, int32_t n_groups, int64_t cols, size_t *bytes) {
     if (!valid_fmt(fmt) || !valid_groups(rows, n_groups) || !bytes || !valid_shape(fmt, rows, cols)) return MXQ_EINVAL;
     if (!grouped_fmt(fmt)) return MXQ_EUNSUPPORTED;
+    if (!valid_grouped_scales(fmt, rows, n_groups, cols)) return MXQ_EINVAL;
     if (fmt_byte_scales(fmt))
         *bytes = (size_t)(grouped_scale_tiles(rows, n_groups) * 128 * round_up(cols / fmt_block(fmt), 16));
     else
@@ -895,6 +901,7 @@ mxq_status mxq_quantize_grouped(const void *x, int32_t xdtype, int64_t x_rows, i
         cols <= 0 || !valid_hadamard(hadamard_b, cols) || !valid_groups(rows, n_groups))
         return MXQ_EINVAL;
     if (!grouped_fmt(fmt)) return MXQ_EUNSUPPORTED;
+    if (!valid_grouped_scales(fmt, rows, n_groups, cols)) return MXQ_EINVAL;
     if (!offsets || !aligned4(offsets) || !aligned4(slot) || topk < 1 || topk > 32 ||
         (!slot && x_rows > 0 && (topk != 1 || x_rows > rows)))
         return MXQ_EINVAL;

@@ -337,10 +337,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gg_threads<F>(), 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + ST * P::kStage);   // (used in the first CTA)
     uint64_t *empty = full + ST;
     uint64_t *accf = empty + ST;      // [2] accumulator stage full
-    uint64_t *acce = accf + 2;               // [2] drained (first CTA)
-    uint64_t *ovlf = acce + 2;               // shared columns drained (first CTA)
+    uint64_t *acce = accf + 2;        // [2] drained (first CTA)
+    uint64_t *ovlf = acce + 2;        // shared columns drained (first CTA)
     uint64_t *drain = ovlf + 1;
-    uint64_t *sfready = drain + 1;           // [ST] a stage's scales in TMEM (first CTA)
+    uint64_t *sfready = drain + 1;    // [ST] a stage's scales in TMEM (first CTA)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sfready + ST);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     Groups &groups = *reinterpret_cast<Groups *>(smem + ST * P::kStage + 256);

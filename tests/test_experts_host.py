@@ -29,7 +29,7 @@ def test_sizes(mxq):
     assert M.expert_weight_bytes(M.INT8_ROW, 2, 10, 64) == (1280, 80)
     assert M.expert_plan_workspace_bytes(4096, 512) == 0
     assert M.expert_plan_workspace_bytes(1 << 22, 512) > 0
-    for bad in ((M.MXFP8, 1, 513, 64), (M.MXFP8, 1, 0, 64), (M.MXFP8, (1 << 22) + 1, 4, 64), (M.MXFP8, -1, 4, 64),
+    for bad in ((M.NVFP4, 512, 512, 1 << 22), (M.MXFP8, 1, 513, 64), (M.MXFP8, 1, 0, 64), (M.MXFP8, (1 << 22) + 1, 4, 64), (M.MXFP8, -1, 4, 64),
                 (M.MXFP8, 4, 4, 48), (9, 4, 4, 64)):
         with pytest.raises(M.MxqError) as e:
             M.grouped_scales_bytes(*bad)

@@ -157,6 +157,25 @@ def test_heads_quantize(mxq, fmt, tokens, hq, hk, d, rot, had, dtype):
         assert near.all(), np.abs(got - want)[~near][:5]
 
 
+@pytest.mark.parametrize("fmt", [MXFP8, MXFP4, INT8_ROW])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("scale", [1.0, 1e-30, 1e-38, 1e-42, 1e15])
+def test_codes_are_those_of_the_fp32_outputs(mxq, fmt, interleaved, scale):
+    """Without the Hadamard rotation the two forms do the same fp32 operations, so the codes have the bits mxq_quantize
+    gives the fp32 outputs: for values whose norm is all eps, subnormal ones, and ones near the largest square."""
+    g = torch.Generator().manual_seed(5)
+    q = (torch.randn(60, 6, 96, generator=g) * scale).cuda()
+    k = (torch.randn(60, 2, 96, generator=g) * scale).cuda()
+    q[3, 1] = 0
+    w = torch.randn(96, generator=g).cuda()
+    cos, sin = (torch.from_numpy(a).cuda() for a in tables(60, 64))
+    plain = mxq.qk_norm_rope(q, k, w, None, cos, sin, norm="layer", interleaved=interleaved)
+    coded = mxq.qk_norm_rope_quantize(q, k, w, None, cos, sin, norm="layer", interleaved=interleaved, fmt=fmt)
+    for p, c in zip(plain, coded):
+        want = mxq.quantize(p.flatten(0, 1), fmt)
+        assert torch.equal(c.codes, want.codes) and torch.equal(c.scales, want.scales)
+
+
 def test_positions_outside_are_reported_and_nan(mxq):
     q = torch.randn(4, 2, 64, device="cuda")
     cos, sin = (torch.from_numpy(a).cuda() for a in tables(10, 64))
