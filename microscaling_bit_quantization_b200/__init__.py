@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -81,14 +82,11 @@ class _ExpertWeightC(ctypes.Structure):
                 ("tensor_scales", ctypes.c_void_p)]
 
 
-class _HeadsC(ctypes.Structure):
-    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
-                ("k_stride", ctypes.c_int64), ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32),
-                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("tokens", ctypes.c_int64),
-                ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
-                ("k_weight", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
-                ("cos_table", ctypes.c_void_p), ("sin_table", ctypes.c_void_p), ("n_positions", ctypes.c_int64),
-                ("positions", ctypes.c_void_p), ("position_bits", ctypes.c_int32)]
+# Descriptors of the calls below, packed with the platform's C layout: building a
+# ctypes structure field by field takes longer than the kernels of a decode step.
+_QTENSOR = struct.Struct("@iiqqPPP")                   # mxq_qtensor
+_EXPERT_WEIGHT = struct.Struct("@iiqqPPP")             # mxq_expert_weight
+_HEADS = struct.Struct("@PPqqiiiiqifPPiiPPqPi")        # mxq_heads
 
 
 def _load():
@@ -147,10 +145,10 @@ def _load():
         "mxq_quantize_grouped": (i32, [P, i32, i64, i64, i32, i32, P, i32, P, i32, i64, P, P, P, P, sz, P]),
         "mxq_expert_weight_bytes": (i32, [i32, i32, i64, i64, psz]),
         "mxq_expert_weight_prepare": (i32, [P, i32, i32, ctypes.POINTER(_ExpertWeightC), P, sz, P]),
-        "mxq_qlinear_grouped": (i32, [ctypes.POINTER(_QTensorC), P, ctypes.POINTER(_ExpertWeightC), P, i32, P]),
+        "mxq_qlinear_grouped": (i32, [P, P, P, P, i32, P]),
         "mxq_expert_combine": (i32, [P, i32, i64, i64, P, P, i64, i32, P, i32, P]),
-        "mxq_qk_norm_rope": (i32, [ctypes.POINTER(_HeadsC), P, i64, P, i64, P]),
-        "mxq_qk_norm_rope_quantize": (i32, [ctypes.POINTER(_HeadsC), i32, i32, P, P, P, P, P]),
+        "mxq_qk_norm_rope": (i32, [P, P, i64, P, i64, P]),
+        "mxq_qk_norm_rope_quantize": (i32, [P, i32, i32, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -676,17 +674,24 @@ def _placed(f):
                 raise ValueError("stream of %s for tensors of %s" % (stream.device, t.device))
             with torch.cuda.stream(stream):
                 return f(x, *args, **kwargs)
-        if index != torch.cuda.current_device():
+        if index != _current_device():
             with torch.cuda.device(index):
                 return f(x, *args, **kwargs)
         return f(x, *args, **kwargs)
     return call
 
 
+# The current device and the current stream's handle, without the objects and
+# checks around them (3 us less per call), where this torch has those calls.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _want(t: Optional[torch.Tensor], what: str, dtype, index: int, shape=None):
-    """The address of a contiguous tensor of device `index`, or None; raises on anything else."""
+    """The address of a contiguous tensor of device `index`, or 0 for None; raises on anything else."""
     if t is None:
-        return None
+        return 0
     if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous() or (shape is not None and t.shape != shape):
         if t.dtype is not dtype:
             raise TypeError("%s: expected %s, got %s" % (what, dtype, t.dtype))
@@ -696,17 +701,12 @@ def _want(t: Optional[torch.Tensor], what: str, dtype, index: int, shape=None):
 
 
 def _bytes(t: Optional[torch.Tensor], what: str, need: int, index: int):
-    """The address of a contiguous tensor of at least `need` bytes, or None where none are needed."""
+    """The address of a contiguous tensor of at least `need` bytes, or 0 where none are needed."""
     if need == 0:
-        return None
+        return 0
     if t is None or t.get_device() != index or not t.is_contiguous() or t.numel() * t.element_size() < need:
         raise ValueError("%s: %d contiguous bytes on device %d are wanted" % (what, need, index))
     return t.data_ptr()
-
-
-# The current stream's handle without a Stream object around it (3 us less per call), where torch has the call.
-_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -795,7 +795,7 @@ def quantize_grouped(x: torch.Tensor, fmt: int, offsets: torch.Tensor, slot: tor
         out = alloc_grouped(fmt, rows, n_groups, cols, x.device)
     codes, scales, ts = _addresses(out, fmt, MMA, rows, n_groups, cols, index, "out")
     wsb = 0
-    if ts is not None:
+    if ts:
         wsb = quantize_workspace_bytes(fmt)
         if workspace is None:
             workspace = torch.empty(wsb, dtype=torch.uint8, device=x.device)
@@ -855,10 +855,10 @@ def qlinear_grouped(xq: QTensor, w: ExpertWeight, offsets: torch.Tensor, out_dty
     index, rows, n, e = xq.codes.get_device(), xq.rows, w.rows, w.n_experts
     if out is None:
         out = torch.empty((rows, n), dtype=out_dtype, device=xq.codes.device)
-    xc = _QTensorC(xq.fmt, xq.layout, rows, xq.cols, *_addresses(xq, xq.fmt, MMA, rows, e, xq.cols, index, "xq"))
+    xc = _QTENSOR.pack(xq.fmt, xq.layout, rows, xq.cols, *_addresses(xq, xq.fmt, MMA, rows, e, xq.cols, index, "xq"))
     cb, sb = expert_weight_bytes(w.fmt, e, n, w.cols)
-    wc = _ExpertWeightC(w.fmt, e, n, w.cols, _bytes(w.codes, "w.codes", cb, index), _bytes(w.scales, "w.scales", sb, index),
-                        _bytes(w.tensor_scales, "w.tensor_scales", 4 * e if w.fmt in (NVFP4, FP8_TENSOR) else 0, index))
+    wc = _EXPERT_WEIGHT.pack(w.fmt, e, n, w.cols, _bytes(w.codes, "w.codes", cb, index), _bytes(w.scales, "w.scales", sb, index),
+                             _bytes(w.tensor_scales, "w.tensor_scales", 4 * e if w.fmt in (NVFP4, FP8_TENSOR) else 0, index))
     _ok(_lib.mxq_qlinear_grouped(xc, _want(offsets, "offsets", torch.int32, index, (e + 1,)), wc,
                                  _want(out, "out", out.dtype, index, (rows, n)), _dtype_code(out), _stream_handle(index)),
         "mxq_qlinear_grouped")
@@ -898,7 +898,7 @@ def _token_stride(x: torch.Tensor, what: str, shape, dtype, index: int) -> int:
     return s[0] if t > 1 else h * d
 
 
-def _heads(q, k, q_weight, k_weight, cos, sin, positions, eps, norm, interleaved) -> _HeadsC:
+def _heads(q, k, q_weight, k_weight, cos, sin, positions, eps, norm, interleaved) -> bytes:
     index, dtype = q.get_device(), q.dtype
     if q.dim() != 3 or k is not None and k.dim() != 3:
         raise ValueError("q and k: [tokens, heads, head_dim] is wanted")
@@ -909,12 +909,13 @@ def _heads(q, k, q_weight, k_weight, cos, sin, positions, eps, norm, interleaved
         raise ValueError("sin: the shape of cos is wanted")
     wide = positions is not None and positions.dtype is torch.int64
     f32 = torch.float32
-    return _HeadsC(q.data_ptr(), None if k is None else k.data_ptr(), _token_stride(q, "q", q.shape, dtype, index),
-                   0 if k is None else _token_stride(k, "k", (tokens, hk, d), dtype, index), hq, hk, d, _dtype_code(q), tokens,
-                   NORMS[norm], eps, _want(q_weight, "q_weight", f32, index, (d,)),
-                   _want(k_weight, "k_weight", f32, index, (d,)), 2 * half, interleaved, _want(cos, "cos", f32, index),
-                   _want(sin, "sin", f32, index), n_pos,
-                   _want(positions, "positions", torch.int64 if wide else torch.int32, index, (tokens,)), 64 if wide else 32)
+    return _HEADS.pack(q.data_ptr(), 0 if k is None else k.data_ptr(), _token_stride(q, "q", q.shape, dtype, index),
+                       0 if k is None else _token_stride(k, "k", (tokens, hk, d), dtype, index), hq, hk, d, _dtype_code(q),
+                       tokens, NORMS[norm], eps, _want(q_weight, "q_weight", f32, index, (d,)),
+                       _want(k_weight, "k_weight", f32, index, (d,)), 2 * half, interleaved,
+                       _want(cos, "cos", f32, index), _want(sin, "sin", f32, index), n_pos,
+                       _want(positions, "positions", torch.int64 if wide else torch.int32, index, (tokens,)),
+                       64 if wide else 32)
 
 
 @_placed

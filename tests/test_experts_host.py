@@ -119,6 +119,23 @@ def test_combine_refusals(mxq):
     assert call(tokens=0, slot=None, out=None) == 0
 
 
+class Heads(ctypes.Structure):   # mxq_heads
+    _fields_ = [("q", P), ("k", P), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("q_heads", ctypes.c_int32),
+                ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("tokens", ctypes.c_int64), ("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("q_weight", P),
+                ("k_weight", P), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("cos_table", P),
+                ("sin_table", P), ("n_positions", ctypes.c_int64), ("positions", P), ("position_bits", ctypes.c_int32)]
+
+
+def test_packed_descriptors_have_the_c_layout(mxq):
+    """What the binding packs is what a C structure of the header's fields holds."""
+    vals = [11, 22, 256, 128, 4, 2, 64, 1, 3, 1, 0.5, 33, 44, 64, 1, 55, 66, 10, 77, 64]
+    assert mxq._HEADS.pack(*vals) == bytes(Heads(*vals))[:mxq._HEADS.size]
+    vals = [2, 1, 5, 64, 11, 22, 33]
+    assert mxq._QTENSOR.pack(*vals) == bytes(mxq._QTensorC(*vals))
+    assert mxq._EXPERT_WEIGHT.pack(*vals) == bytes(mxq._ExpertWeightC(*vals))
+
+
 def test_heads_refusals(mxq):
     M, L = mxq, mxq.lib()
     good = dict(q=D, k=D, q_stride=256, k_stride=256, q_heads=4, k_heads=2, head_dim=64, dtype=1, tokens=3, norm=0, eps=1e-6,
@@ -126,11 +143,11 @@ def test_heads_refusals(mxq):
                 positions=None, position_bits=32)
 
     def plain(qo=D, qs=256, ko=D, ks=128, **more):
-        h = M._HeadsC(**{**good, **more})
+        h = Heads(**{**good, **more})
         return L.mxq_qk_norm_rope(ctypes.byref(h), qo, qs, ko, ks, None)
 
     def coded(fmt=0, had=0, qc=D, qs=D, kc=D, ks=D, **more):
-        h = M._HeadsC(**{**good, **more})
+        h = Heads(**{**good, **more})
         return L.mxq_qk_norm_rope_quantize(ctypes.byref(h), fmt, had, qc, qs, kc, ks, None)
 
     shared = (dict(q=None), dict(q=D + 8), dict(q_stride=260), dict(q_stride=248), dict(k_stride=120), dict(k=None), dict(head_dim=60),
