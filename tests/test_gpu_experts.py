@@ -438,3 +438,50 @@ def test_stream_argument(mxq):
     a, b = mxq.expert_plan(ids, 4, stream=s), mxq.expert_plan(ids, 4)
     torch.cuda.synchronize()
     assert torch.equal(a.offsets, b.offsets) and torch.equal(a.slot, b.slot)
+
+
+def test_plan_of_many_choices_captured(mxq):
+    """The two-kernel plan, its workspace from the graph's own pool, replayed on other ids."""
+    ids = torch.randint(0, 300, (20000, 2), device="cuda", dtype=torch.int32)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, capture_error_mode="thread_local"):
+        plan = mxq.expert_plan(ids, 300)
+    for _ in range(3):
+        ids.copy_(torch.randint(-3, 310, (20000, 2), device="cuda", dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        off, slot = ref_plan(ids.cpu().numpy(), 300)
+        np.testing.assert_array_equal(plan.offsets.cpu().numpy(), off)
+        np.testing.assert_array_equal(plan.slot.cpu().numpy(), slot)
+    check_plan(mxq, np.random.default_rng(1).integers(0, 512, (1 << 19, 8)), 512, torch.int64)   # the most choices there can be
+
+
+@pytest.mark.parametrize("fmt", [MXFP8, INT8_ROW])
+def test_rows_past_32_bits(mxq, orc, fmt):
+    """Codes of 2.5 GB and products of 4.9 GB: the last rows against the oracle."""
+    tokens, topk, e, n, k = 300000, 2, 4, 4096, 4096
+    torch.manual_seed(fmt)
+    x = torch.empty(tokens, k, dtype=torch.bfloat16, device="cuda")
+    x.normal_()
+    w = torch.randn(e, n, k, device="cuda") * 0.02
+    ids = torch.stack([torch.arange(tokens, device="cuda") % 2, 2 + torch.arange(tokens, device="cuda") % 2], 1)
+    plan = mxq.expert_plan(ids, e)
+    xq = mxq.quantize_grouped(x, fmt, plan.offsets, plan.slot)
+    y = mxq.qlinear_grouped(xq, mxq.prepare_experts(w, fmt), plan.offsets)
+    gate = torch.rand(tokens, topk, device="cuda")
+    out = mxq.expert_combine(y, plan.slot, gate)
+    assert mxq.check() == 0
+    pick = np.array([0, 1, 131071, 262144, tokens - 2, tokens - 1])
+    xv = deq64(orc.quantize(x[pick].float().cpu().numpy(), fmt))
+    wv = [deq64(orc.quantize(w[i].cpu().numpy(), fmt)) for i in range(e)]
+    slot = plan.slot[pick].cpu().numpy()
+    assert slot.max() >= tokens * topk - 2
+    for i, t in enumerate(pick):
+        both = [xv[i] @ wv[t % 2].T, xv[i] @ wv[2 + t % 2].T]
+        for j in range(2):
+            gemm_close(y[slot[i, j]].float().cpu().numpy(), both[j], bf16_out=True)
+        wt = gate[t].cpu().numpy().astype(np.float64)
+        mag = wt[0] * np.abs(both[0]) + wt[1] * np.abs(both[1])
+        ref = wt[0] * both[0] + wt[1] * both[1]
+        assert (np.abs(out[t].float().cpu().numpy() - ref) <= 2.0 ** -8 * (mag + np.abs(ref)) + 2e-4 * np.abs(both).max()).all()

@@ -214,3 +214,23 @@ def test_empty_zero_rows_and_graph(mxq):
     again = mxq.qk_norm_rope(x, x, None, None, cos, sin, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(again[0], want[0]) and mxq.check() == 0
+
+
+@pytest.mark.parametrize("fmt", [None, MXFP8])
+def test_tokens_past_32_bits(mxq, fmt):
+    """2.5 G elements: the last tokens as a call on them alone gives them."""
+    t, hq, hk, d = 480000, 32, 8, 128
+    x = torch.empty(t, hq + hk, d, dtype=torch.bfloat16, device="cuda")
+    x.normal_()
+    q, k = x[:, :hq], x[:, hq:]
+    cos, sin = (torch.from_numpy(a).cuda() for a in tables(100, d))
+    pos = torch.arange(t, device="cuda") % 100
+    f = mxq.qk_norm_rope if fmt is None else lambda *a: mxq.qk_norm_rope_quantize(*a, fmt=fmt, hadamard_b=d)
+    big = f(q, k, None, None, cos, sin, pos)
+    tail = f(q[-5:], k[-5:], None, None, cos, sin, pos[-5:])
+    assert mxq.check() == 0
+    for b, s, h in zip(big, tail, (hq, hk)):
+        if fmt is None:
+            assert torch.equal(b[-5:], s)
+        else:
+            assert torch.equal(b.codes[-5 * h * d:], s.codes) and torch.equal(b.scales[-5 * h * d // 32:], s.scales)
