@@ -524,9 +524,11 @@ __global__ void __launch_bounds__(kGqThreads) k_quantize_grouped_int8(const T *_
 // ------------------------------------------------------------------ combine
 //
 // out[t] = sum over i of weights[t][i] y[slot[t][i]], fp32 FMAs in the order
-// of i.  A warp owns up to 1024 neighbouring columns of a token; lane i reads
-// choice i's row and weight once, and a lane has eight 16-byte loads (four
-// vectors of two rows) in flight.  Bound: HBM.
+// of i.  A warp owns up to 1024 neighbouring columns of a token (with few
+// tokens 256); lane i reads choice i's row and weight once, and a lane has eight
+// 16-byte loads in flight, four vectors of two rows or one of eight.
+// Bound: HBM (16,384 tokens x 4 x 4096 in bf16: 98 us, 6.7 TB/s; two rows of
+// eight columns a thread, addressed one by one, took 142).
 
 struct CombineArgs {
     int64_t rows, n;
@@ -537,8 +539,6 @@ struct CombineArgs {
     int topk;
     unsigned int *err;
 };
-constexpr int kCombineSteps = 4;   // vectors of a lane: a warp takes 128 neighbouring ones of a token
-
 template <typename T, int V>
 struct Vec;
 template <>
@@ -588,13 +588,15 @@ __device__ __forceinline__ void store_vec(float *p, const float (&v)[8]) {
 __device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&v)[1]) { *p = __float2bfloat16_rn(v[0]); }
 __device__ __forceinline__ void store_vec(float *p, const float (&v)[1]) { *p = v[0]; }
 
-template <typename T, typename O, int V>
-__global__ void __launch_bounds__(256) k_expert_combine(const T *__restrict__ y, O *__restrict__ out, CombineArgs a) {
+// STEPS vectors of a lane (a warp takes 32 STEPS neighbouring ones of a token),
+// ROWS choices at a time: all their loads before any use.
+template <typename T, typename O, int V, int STEPS, int ROWS>
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) k_expert_combine(const T *__restrict__ y, O *__restrict__ out, CombineArgs a) {
     const int lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
     for (uint32_t u = blockIdx.x * 8 + (threadIdx.x >> 5); u < a.units; u += gridDim.x * 8) {
-        const uint32_t t = fdiv(u, a.segs), c0 = (u - t * a.n_segs) * (32 * kCombineSteps) + lane;
+        const uint32_t t = fdiv(u, a.segs), c0 = (u - t * a.n_segs) * (32 * STEPS) + lane;
         int row = -1;   // lane i: choice i's row and weight
         float weight = 1.0f;
         if (lane < a.topk) {
@@ -606,38 +608,35 @@ __global__ void __launch_bounds__(256) k_expert_combine(const T *__restrict__ y,
             }
         }
         unsigned left = __ballot_sync(0xFFFFFFFFu, row >= 0);
-        float acc[kCombineSteps][V] = {};
-        while (left) {   // two rows at a time, all their loads before any use
-            const int i0 = __ffs(left) - 1;
-            left &= left - 1;
-            const int i1 = left ? __ffs(left) - 1 : -1;
-            left &= left - 1;
-            const T *y0 = y + (int64_t)__shfl_sync(0xFFFFFFFFu, row, i0) * a.n;
-            const T *y1 = y + (int64_t)__shfl_sync(0xFFFFFFFFu, row, i1 < 0 ? i0 : i1) * a.n;
-            const float w0 = __shfl_sync(0xFFFFFFFFu, weight, i0), w1 = __shfl_sync(0xFFFFFFFFu, weight, i1 < 0 ? i0 : i1);
-            Vec<T, V> q0[kCombineSteps], q1[kCombineSteps];
+        float acc[STEPS][V] = {};
+        while (left) {
+            Vec<T, V> q[ROWS][STEPS];
+            float w[ROWS];
+            bool on[ROWS];
 #pragma unroll
-            for (int k = 0; k < kCombineSteps; k++)
-                if (c0 + 32 * k < a.n_vec) {
-                    q0[k].load(y0 + (int64_t)(c0 + 32 * k) * V);
-                    if (i1 >= 0) q1[k].load(y1 + (int64_t)(c0 + 32 * k) * V);
-                }
+            for (int i = 0; i < ROWS; i++) {
+                on[i] = left != 0;
+                const int choice = on[i] ? __ffs(left) - 1 : 0;
+                left &= left - 1;
+                w[i] = __shfl_sync(0xFFFFFFFFu, weight, choice);
+                const T *from = y + (int64_t)__shfl_sync(0xFFFFFFFFu, row, choice) * a.n;
 #pragma unroll
-            for (int k = 0; k < kCombineSteps; k++)
-                if (c0 + 32 * k < a.n_vec) {
-                    float v[V];
-                    q0[k].get(v);
+                for (int k = 0; k < STEPS; k++)
+                    if (on[i] && c0 + 32 * k < a.n_vec) q[i][k].load(from + (int64_t)(c0 + 32 * k) * V);
+            }
 #pragma unroll
-                    for (int j = 0; j < V; j++) acc[k][j] = __fmaf_rn(w0, v[j], acc[k][j]);
-                    if (i1 >= 0) {
-                        q1[k].get(v);
+            for (int i = 0; i < ROWS; i++)
 #pragma unroll
-                        for (int j = 0; j < V; j++) acc[k][j] = __fmaf_rn(w1, v[j], acc[k][j]);
+                for (int k = 0; k < STEPS; k++)
+                    if (on[i] && c0 + 32 * k < a.n_vec) {
+                        float v[V];
+                        q[i][k].get(v);
+#pragma unroll
+                        for (int j = 0; j < V; j++) acc[k][j] = __fmaf_rn(w[i], v[j], acc[k][j]);
                     }
-                }
         }
 #pragma unroll
-        for (int k = 0; k < kCombineSteps; k++)
+        for (int k = 0; k < STEPS; k++)
             if (c0 + 32 * k < a.n_vec) store_vec(out + (int64_t)t * a.n + (int64_t)(c0 + 32 * k) * V, acc[k]);
     }
 }
@@ -699,11 +698,19 @@ cudaError_t quantize_grouped(const T *x, int fmt, GroupedQuantArgs a, cudaStream
 }
 
 template <typename T, typename O, int V>
-cudaError_t combine(const void *y, void *out, const CombineArgs &a, cudaStream_t s) {
+cudaError_t combine(const void *y, void *out, CombineArgs a, int64_t tokens, cudaStream_t s) {
+    // four vectors a lane where that still gives every SM 16 warps, else one
+    // (32 tokens x 8 x 4096: 4.8 us with four, 2.1 with one)
+    const int64_t wide = (a.n_vec + 127) / 128, sms = sm_count();
+    const bool few = tokens * wide < sms * 16;
+    const int64_t segs = few ? (a.n_vec + 31) / 32 : wide;
+    a.segs = make_fastdiv((uint32_t)segs);
+    a.n_segs = (uint32_t)segs;
+    a.units = (uint32_t)(tokens * segs);
     int64_t ctas = ((int64_t)a.units + 7) / 8;
-    const int64_t cap = (int64_t)sm_count() * 64;
-    if (ctas > cap) ctas = cap;
-    return launch_pdl(k_expert_combine<T, O, V>, ctas, 256, s, (const T *)y, (O *)out, a);
+    if (ctas > sms * 64) ctas = sms * 64;
+    if (few) return launch_pdl(k_expert_combine<T, O, V, 1, 8>, ctas, 256, s, (const T *)y, (O *)out, a);
+    return launch_pdl(k_expert_combine<T, O, V, 4, 2>, ctas, 256, s, (const T *)y, (O *)out, a);
 }
 
 }  // namespace
@@ -759,10 +766,6 @@ cudaError_t launch_expert_combine(const void *y, bool y_bf16, int64_t rows, int6
     const int64_t per_row = vec ? n / 8 : n;
     a.rows = rows;
     a.n = n;
-    const int64_t segs = (per_row + 32 * kCombineSteps - 1) / (32 * kCombineSteps);
-    a.segs = make_fastdiv((uint32_t)segs);
-    a.n_segs = (uint32_t)segs;
-    a.units = (uint32_t)(tokens * segs);
     a.n_vec = (uint32_t)per_row;
     a.slot = slot;
     a.weights = weights;
@@ -771,11 +774,11 @@ cudaError_t launch_expert_combine(const void *y, bool y_bf16, int64_t rows, int6
     if (e != cudaSuccess) return e;
     using bf = __nv_bfloat16;
     if (y_bf16) {
-        if (out_bf16) return vec ? combine<bf, bf, 8>(y, out, a, s) : combine<bf, bf, 1>(y, out, a, s);
-        return vec ? combine<bf, float, 8>(y, out, a, s) : combine<bf, float, 1>(y, out, a, s);
+        if (out_bf16) return vec ? combine<bf, bf, 8>(y, out, a, tokens, s) : combine<bf, bf, 1>(y, out, a, tokens, s);
+        return vec ? combine<bf, float, 8>(y, out, a, tokens, s) : combine<bf, float, 1>(y, out, a, tokens, s);
     }
-    if (out_bf16) return vec ? combine<float, bf, 8>(y, out, a, s) : combine<float, bf, 1>(y, out, a, s);
-    return vec ? combine<float, float, 8>(y, out, a, s) : combine<float, float, 1>(y, out, a, s);
+    if (out_bf16) return vec ? combine<float, bf, 8>(y, out, a, tokens, s) : combine<float, bf, 1>(y, out, a, tokens, s);
+    return vec ? combine<float, float, 8>(y, out, a, tokens, s) : combine<float, float, 1>(y, out, a, tokens, s);
 }
 
 }  // namespace mxq
