@@ -752,7 +752,7 @@ typedef struct mxq_heads {
     int32_t q_heads, k_heads;
     int32_t head_dim;              /* multiple of 8, 8 .. 256                 */
     int32_t dtype;                 /* mxq_dtype of q and k                    */
-    int64_t tokens;
+    int64_t tokens;                /* below 2^30                              */
     int32_t norm;                  /* mxq_norm                                */
     float eps;
     const float *q_weight, *k_weight;   /* device fp32[head_dim] or NULL (all 1) */
@@ -768,7 +768,8 @@ typedef struct mxq_heads {
  *   v = x / sqrt(mean(x^2) + eps) * weight   (MXQ_NORM_LAYER: x - mean(x)
  *   for x, the mean square of that), then for the pairs (a, b) of the first
  *   rot_dim elements a' = a c - b s, b' = b c + a s with c, s of the token's
- *   position and pair; fp32, rounded once (RNE) for bf16.
+ *   position and pair; fp32, rounded once (RNE) for bf16 (sums of squares, and
+ *   products of an element and its weight, beyond 3.4e38 overflow).
  *   q_out, k_out: device, dtype of h, strides in elements as q and k; q_out
  *     may be q (same stride), k_out may be k.
  * A position outside [0, n_positions) makes its token's heads NaN and is

@@ -1027,7 +1027,7 @@ static mxq_status check_heads(const mxq_heads *h, HeadArgs *a) {
         h->rot_dim > h->head_dim || h->rot_dim % 8 || (h->norm != MXQ_NORM_RMS && h->norm != MXQ_NORM_LAYER) ||
         !(h->eps >= 0.0f))
         return MXQ_EINVAL;
-    if (h->tokens > ((int64_t)1 << 40)) return MXQ_EINVAL;
+    if (h->tokens >= ((int64_t)1 << 30)) return MXQ_EINVAL;   // the items of q and k are counted in 31 bits
     if (h->positions && h->position_bits != 32 && h->position_bits != 64) return MXQ_EINVAL;
     if (h->positions && (reinterpret_cast<uintptr_t>(h->positions) & (uintptr_t)(h->position_bits / 8 - 1))) return MXQ_EINVAL;
     if (h->rot_dim > 0 && h->tokens > 0) {

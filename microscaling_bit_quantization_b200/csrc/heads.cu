@@ -541,11 +541,11 @@ cudaError_t launch_qk_norm_rope(const HeadArgs &h, cudaStream_t s) {
     a.units = h.head_dim / 8;
     a.per_pass = 32 / a.units;
     // Few tokens: a token's heads are spread over warps, down to one pass each;
-    // many: a warp does up to 16 passes and reads its angles once.
+    // many: a warp does up to kHeadPasses passes and reads its angles once.
     const int64_t qp = (h.q_heads + a.per_pass - 1) / a.per_pass, kp = (h.k_heads + a.per_pass - 1) / a.per_pass;
     int64_t per = h.tokens * (qp + kp) / ((int64_t)sm_count() * 16);
     per = per < 1 ? 1 : per > kHeadPasses ? kHeadPasses : per;
-    while (h.tokens * ((qp + per - 1) / per + (kp + per - 1) / per) >= ((int64_t)1 << 31)) per *= 2;   // items are counted in 31 bits
+    while (h.tokens * ((qp + per - 1) / per + (kp + per - 1) / per) >= ((int64_t)1 << 31)) per *= 2;   // items are counted in 31 bits (tokens in 30: two items of a token fit)
     a.per_item = (int)per;
     a.q_items = (int)((qp + per - 1) / per);
     const int64_t items = a.q_items + (kp + per - 1) / per;

@@ -165,6 +165,10 @@ def test_heads_refusals(mxq):
         assert coded(**bad) == EINVAL, bad
     for fmt in (M.NVFP4, M.INT4_G32, M.INT4_G64, M.FP8_TENSOR):
         assert coded(fmt=fmt) == EUNSUPPORTED
+    for tokens in (1 << 30, (1 << 31) + 1, 1 << 40, (1 << 63) - 1):   # items of tokens and sides are counted in 31 bits
+        many = dict(tokens=tokens, rot_dim=0, cos_table=None, sin_table=None)
+        assert plain(**many) == EINVAL and coded(**many) == EINVAL, tokens
+        assert plain(**many, k_heads=0, k=None) == EINVAL, tokens
     assert plain(tokens=0, q=None, k=None, qo=None, ko=None) == 0
     assert L.mxq_qk_norm_rope(None, D, 256, D, 128, None) == EINVAL
 
