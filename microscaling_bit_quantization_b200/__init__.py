@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 import struct
 from dataclasses import dataclass
@@ -663,9 +664,15 @@ def qlinear_mixed(xq: QTensor, mw: MixedWeight, out_dtype=torch.bfloat16, out: t
 
 def _placed(f):
     """Runs f with its first tensor's device, and `stream`, as the current ones."""
+    sig = inspect.signature(f)
+    first = next(iter(sig.parameters))
+
     @functools.wraps(f)
-    def call(x, *args, stream=None, **kwargs):
-        t = x.codes if type(x) is QTensor else x
+    def call(*args, stream=None, **kwargs):
+        if not args and first not in kwargs:
+            raise TypeError("%s: %s is missing" % (f.__name__, first))
+        x = args[0] if args else kwargs[first]
+        t = x.codes if isinstance(x, QTensor) else x
         index = t.get_device()
         if index < 0:
             raise ValueError("tensors must be on a CUDA device (there is no CPU path)")
@@ -673,11 +680,13 @@ def _placed(f):
             if stream.device != t.device:
                 raise ValueError("stream of %s for tensors of %s" % (stream.device, t.device))
             with torch.cuda.stream(stream):
-                return f(x, *args, **kwargs)
+                return f(*args, **kwargs)
         if index != _current_device():
             with torch.cuda.device(index):
-                return f(x, *args, **kwargs)
-        return f(x, *args, **kwargs)
+                return f(*args, **kwargs)
+        return f(*args, **kwargs)
+    call.__signature__ = sig.replace(parameters=[*sig.parameters.values(), inspect.Parameter(
+        "stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return call
 
 

@@ -181,3 +181,19 @@ def test_cpu_tensors_are_refused(mxq):
         mxq.qk_norm_rope(torch.zeros(2, 2, 64))
     with pytest.raises(ValueError):
         mxq.expert_combine(torch.zeros(2, 64), torch.zeros(1, 2, dtype=torch.int32))
+
+
+def test_first_argument_by_name(mxq):
+    """Every call takes its first tensor by name too, and says what it takes."""
+    import inspect
+    import torch
+    x = torch.zeros(2, 2, 64)
+    for f, kw in ((mxq.expert_plan, dict(expert_ids=x, n_experts=4)), (mxq.quantize_grouped, dict(x=x, fmt=0, offsets=x)),
+                  (mxq.prepare_experts, dict(w=x, fmt=0)), (mxq.expert_combine, dict(y=x, slot=x)),
+                  (mxq.qk_norm_rope, dict(q=x, k=x)), (mxq.qk_norm_rope_quantize, dict(q=x)),
+                  (mxq.qlinear_grouped, dict(xq=mxq.QTensor(0, mxq.MMA, 2, 64, x, None, None), w=None, offsets=x))):
+        with pytest.raises(ValueError, match="CUDA device"):   # reached the check of the device
+            f(**kw)
+        assert list(inspect.signature(f).parameters)[0] in kw and "stream" in inspect.signature(f).parameters
+        with pytest.raises(TypeError, match="missing"):
+            f()
