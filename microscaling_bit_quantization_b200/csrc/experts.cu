@@ -460,6 +460,9 @@ __global__ void __launch_bounds__(kGqThreads) k_quantize_grouped_int8(const T *_
     pdl_wait();
     pdl_launch_dependents();
     const int first = clamp_row(a.offsets[0], a.rows), last = clamp_row(a.offsets[a.n_groups], a.rows);
+    if (blockIdx.x == 0)   // no scale needs a row's group here: the offsets between are only checked
+        for (int i = threadIdx.x; i <= a.n_groups; i += kGqThreads)
+            if (offset_wrong(a.offsets, i, a.rows)) latch_index_error(a.err);
     const float norm = a.hadamard_b ? __frsqrt_rn((float)a.hadamard_b) : 1.0f;
     const uint32_t cpr = (uint32_t)(a.cols >> 4), steps = (cpr + 31) / 32;
     for (uint32_t t = blockIdx.x * kGqWarps + (threadIdx.x >> 5); t < (uint32_t)a.x_rows; t += gridDim.x * kGqWarps) {

@@ -23,6 +23,12 @@ __device__ __forceinline__ int clamp_row(int o, int64_t rows) {
     return o < 0 ? 0 : (int64_t)o > rows ? (int)rows : o;
 }
 
+// Whether offsets[i] lies outside [0, rows] or before its predecessor.
+__device__ __forceinline__ bool offset_wrong(const int32_t *offsets, int i, int64_t rows) {
+    const int o = offsets[i];
+    return o != clamp_row(o, rows) || (i > 0 && offsets[i - 1] > o);
+}
+
 struct Groups {
     int off[kMaxGroups + 1];
     int tile[kMaxGroups + 1];   // 128-row scale tiles before each group
@@ -33,9 +39,8 @@ struct Groups {
 // clamped is reported to *err when err is given.
 __device__ __forceinline__ void load_groups(Groups &g, const int32_t *offsets, int n, int64_t rows, unsigned int *err) {
     for (int i = threadIdx.x; i <= n; i += blockDim.x) {
-        const int o = offsets[i];
-        g.off[i] = clamp_row(o, rows);
-        if (o != g.off[i] || (i > 0 && offsets[i - 1] > o)) latch_index_error(err);
+        g.off[i] = clamp_row(offsets[i], rows);
+        if (offset_wrong(offsets, i, rows)) latch_index_error(err);
     }
     __syncthreads();
     if (threadIdx.x < 32) {

@@ -161,6 +161,19 @@ def test_quantize_grouped(mxq, orc, fmt, tokens, topk, n, cols, had, dtype):
             np.testing.assert_array_equal(a[finite], b[finite])
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("off", [[0, 6, 3, 8], [0, 3, 6, 9], [-1, 3, 6, 8]])
+def test_quantize_reports_wrong_offsets(mxq, fmt, off):
+    """Offsets out of order or outside the 8 rows: reported by every format, nothing written past the buffers."""
+    x = torch.ones((8, 64), dtype=torch.bfloat16, device="cuda")
+    q = filled(mxq, fmt, 8, 3, 64)
+    guard = torch.full((q.codes.numel() + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    q.codes = guard[:q.codes.numel()]
+    mxq.quantize_grouped(x, fmt, torch.tensor(off, dtype=torch.int32, device="cuda"), out=q)
+    assert mxq.check() == 1 and mxq.check() == 0
+    assert (guard[q.codes.numel():] == 0xAB).all()
+
+
 class Bits:
     def __init__(self, codes, scales, tensor_scale, rows):
         self.codes, self.scales, self.tensor_scale, self.rows = codes, scales, tensor_scale, rows
@@ -318,7 +331,7 @@ def test_offsets_out_of_order_are_clamped_and_reported(mxq, orc, bad, fmt, scale
     q = mxq.alloc_grouped(fmt, 20 * scale, 3, 256)
     x = torch.randn(20 * scale, 256, device="cuda")
     mxq.quantize_grouped(x, fmt, off, out=q)
-    assert mxq.check() == (0 if fmt == INT8_ROW else 1) and mxq.check() == 0
+    assert mxq.check() == 1 and mxq.check() == 0
     ex.check(mxq, torch.float32)
 
 
