@@ -719,20 +719,27 @@ def _bytes(t: Optional[torch.Tensor], what: str, need: int, index: int):
 
 
 @functools.lru_cache(maxsize=1024)
-def _sizes(fmt: int, layout: int, rows: int, n_groups: int, cols: int):
-    """Bytes of codes, scales (grouped when n_groups) and tensor scale."""
+def _sizes(fmt: int, layout: int, rows: int, n_groups: Optional[int], cols: int):
+    """Bytes of codes, scales (grouped unless n_groups is None) and tensor scale."""
     return (codes_bytes(fmt, rows, cols, layout),
-            grouped_scales_bytes(fmt, rows, n_groups, cols) if n_groups else scales_bytes(fmt, rows, cols, layout),
+            scales_bytes(fmt, rows, cols, layout) if n_groups is None else grouped_scales_bytes(fmt, rows, n_groups, cols),
             4 if fmt in (NVFP4, FP8_TENSOR) else 0)
 
 
-def _addresses(q: QTensor, fmt: int, layout: int, rows: int, n_groups: int, cols: int, index: int, what: str):
+def _addresses(q: QTensor, fmt: int, layout: int, rows: int, n_groups: Optional[int], cols: int, index: int, what: str):
     """Checks a QTensor against what a call needs; its three addresses."""
     if q.fmt != fmt or q.layout != layout or q.rows != rows or q.cols != cols:
         raise ValueError("%s: a %s tensor of %d x %d in layout %d is wanted" % (what, FORMAT_NAMES.get(fmt, fmt), rows, cols, layout))
     c, s, t = _sizes(fmt, layout, rows, n_groups, cols)
     return (_bytes(q.codes, what + ".codes", c, index), _bytes(q.scales, what + ".scales", s, index),
             _bytes(q.tensor_scale, what + ".tensor_scale", t, index))
+
+
+def _alloc(fmt: int, layout: int, rows: int, n_groups: Optional[int], cols: int, device) -> QTensor:
+    c, s, t = _sizes(fmt, layout, rows, n_groups, cols)
+    return QTensor(fmt, layout, rows, cols, torch.empty(c, dtype=torch.uint8, device=device),
+                   torch.empty(s, dtype=torch.uint8, device=device) if s else None,
+                   torch.empty(1, dtype=torch.float32, device=device) if t else None)
 
 
 @dataclass
@@ -755,16 +762,18 @@ def expert_plan(expert_ids: torch.Tensor, n_experts: int, out: ExpertPlan = None
     wide = ids.dtype is torch.int64
     if not wide and ids.dtype is not torch.int32 or ids.dim() != 2:
         raise TypeError("expert_ids: a 2-D int32 or int64 tensor is wanted")
-    rows, shape = ids.numel(), ids.shape
+    rows = ids.numel()
     if out is None:
         out = ExpertPlan(torch.empty(n_experts + 1, dtype=torch.int32, device=ids.device),
-                         torch.empty(shape, dtype=torch.int32, device=ids.device))
+                         torch.empty_like(ids, dtype=torch.int32))
+        offsets, slot = out.offsets.data_ptr(), out.slot.data_ptr()
+    else:
+        offsets = _want(out.offsets, "offsets", torch.int32, index, (n_experts + 1,))
+        slot = _want(out.slot, "slot", torch.int32, index, ids.shape)
     need = _plan_bytes(rows, n_experts)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
-    _ok(_lib.mxq_expert_plan(ids.data_ptr(), 64 if wide else 32, rows, n_experts,
-                             _want(out.offsets, "offsets", torch.int32, index, (n_experts + 1,)),
-                             _want(out.slot, "slot", torch.int32, index, shape),
+    _ok(_lib.mxq_expert_plan(ids.data_ptr(), 64 if wide else 32, rows, n_experts, offsets, slot,
                              _bytes(workspace, "workspace", need, index), need, _stream_handle(index)), "mxq_expert_plan")
     return out
 
@@ -778,10 +787,7 @@ def grouped_scales_bytes(fmt: int, rows: int, n_groups: int, cols: int) -> int:
 
 def alloc_grouped(fmt: int, rows: int, n_groups: int, cols: int, device="cuda") -> QTensor:
     """Buffers of `rows` rows in expert order (layout MMA, scales in the grouped layout)."""
-    sb = grouped_scales_bytes(fmt, rows, n_groups, cols)
-    return QTensor(fmt, MMA, rows, cols, torch.empty(codes_bytes(fmt, rows, cols, MMA), dtype=torch.uint8, device=device),
-                   torch.empty(sb, dtype=torch.uint8, device=device) if sb else None,
-                   torch.empty(1, dtype=torch.float32, device=device) if fmt in (NVFP4, FP8_TENSOR) else None)
+    return _alloc(fmt, MMA, rows, n_groups, cols, device)
 
 
 @_placed
@@ -863,7 +869,7 @@ def qlinear_grouped(xq: QTensor, w: ExpertWeight, offsets: torch.Tensor, out_dty
     """y[r] = deq(xq)[r] . deq(w[expert of row r])^T for the rows of every expert; other rows of `out` stay."""
     index, rows, n, e = xq.codes.get_device(), xq.rows, w.rows, w.n_experts
     if out is None:
-        out = torch.empty((rows, n), dtype=out_dtype, device=xq.codes.device)
+        out = torch.empty(rows, n, dtype=out_dtype, device=xq.codes.device)
     xc = _QTENSOR.pack(xq.fmt, xq.layout, rows, xq.cols, *_addresses(xq, xq.fmt, MMA, rows, e, xq.cols, index, "xq"))
     cb, sb = expert_weight_bytes(w.fmt, e, n, w.cols)
     wc = _EXPERT_WEIGHT.pack(w.fmt, e, n, w.cols, _bytes(w.codes, "w.codes", cb, index), _bytes(w.scales, "w.scales", sb, index),
@@ -884,7 +890,7 @@ def expert_combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = 
     rows, n = y.shape
     tokens, topk = slot.shape
     if out is None:
-        out = torch.empty((tokens, n), dtype=out_dtype or y.dtype, device=y.device)
+        out = torch.empty(tokens, n, dtype=out_dtype or y.dtype, device=y.device)
     _ok(_lib.mxq_expert_combine(_want(y, "y", y.dtype, index), _dtype_code(y), rows, n,
                                 _want(slot, "slot", torch.int32, index),
                                 _want(weights, "weights", torch.float32, index, (tokens, topk)), tokens, topk,
@@ -898,10 +904,11 @@ def expert_combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = 
 
 def _token_stride(x: torch.Tensor, what: str, shape, dtype, index: int) -> int:
     """Elements between the tokens of [tokens, heads, dim] whose heads lie one after the other."""
-    t, h, d = shape
-    s = x.stride()
-    if x.shape != shape or x.dtype is not dtype or x.get_device() != index or len(s) != 3 or \
-            d > 1 and s[2] != 1 or h > 1 and s[1] != d:
+    if x.shape != shape or x.dtype is not dtype or x.get_device() != index:
+        s = None
+    else:
+        s, (t, h, d) = x.stride(), shape
+    if s is None or d > 1 and s[2] != 1 or h > 1 and s[1] != d:
         raise ValueError("%s: %s %s on device %d with the heads of a token one after the other is wanted" %
                          (what, dtype, tuple(shape), index))
     return s[0] if t > 1 else h * d
@@ -937,9 +944,9 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor = None, q_weight: torch.Tensor
     (q_out, k_out)."""
     h = _heads(q, k, q_weight, k_weight, cos, sin, positions, eps, norm, interleaved)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
     index = q.get_device()
     _ok(_lib.mxq_qk_norm_rope(h, q_out.data_ptr(), _token_stride(q_out, "q_out", q.shape, q.dtype, index),
                               None if k is None else k_out.data_ptr(),
@@ -960,13 +967,13 @@ def qk_norm_rope_quantize(q: torch.Tensor, k: torch.Tensor = None, q_weight: tor
     h = _heads(q, k, q_weight, k_weight, cos, sin, positions, eps, norm, interleaved)
     index, d = q.get_device(), q.shape[2]
     if q_out is None:
-        q_out = alloc_qtensor(fmt, q.shape[0] * q.shape[1], d, CANONICAL, q.device)
-    qc, qs, _ = _addresses(q_out, fmt, CANONICAL, q.shape[0] * q.shape[1], 0, d, index, "q_out")
+        q_out = _alloc(fmt, CANONICAL, q.shape[0] * q.shape[1], None, d, q.device)
+    qc, qs, _ = _addresses(q_out, fmt, CANONICAL, q.shape[0] * q.shape[1], None, d, index, "q_out")
     kc = ks = None
     if k is not None:
         if k_out is None:
-            k_out = alloc_qtensor(fmt, k.shape[0] * k.shape[1], d, CANONICAL, k.device)
-        kc, ks, _ = _addresses(k_out, fmt, CANONICAL, k.shape[0] * k.shape[1], 0, d, index, "k_out")
+            k_out = _alloc(fmt, CANONICAL, k.shape[0] * k.shape[1], None, d, k.device)
+        kc, ks, _ = _addresses(k_out, fmt, CANONICAL, k.shape[0] * k.shape[1], None, d, index, "k_out")
     _ok(_lib.mxq_qk_norm_rope_quantize(h, fmt, hadamard_b, qc, qs, kc, ks, _stream_handle(index)), "mxq_qk_norm_rope_quantize")
     return q_out, (k_out if k is not None else None)
 

@@ -197,3 +197,9 @@ def test_first_argument_by_name(mxq):
         assert list(inspect.signature(f).parameters)[0] in kw and "stream" in inspect.signature(f).parameters
         with pytest.raises(TypeError, match="missing"):
             f()
+
+
+def test_alloc_refuses_no_groups(mxq):
+    for n in (0, -1, 513):
+        with pytest.raises(mxq.MxqError):
+            mxq.alloc_grouped(mxq.MXFP8, 4, n, 64, device="cpu")
