@@ -33,16 +33,17 @@ namespace {
 
 constexpr int kHeadThreads = 128;
 constexpr int kHeadWarps = kHeadThreads / 32;
-constexpr int kHeadPasses = 8;   // of an item, at most
+constexpr int kHeadPasses = 16;   // of an item, at most
 
 struct HeadKernelArgs {
     HeadArgs h;
     int units;          // lanes per head
     int per_pass;       // heads a warp takes at a time
-    int per_item;       // such passes that make an item, a warp's work; an item lies on one side, q or k
-    int q_items;        // of a token, then those of its k heads
-    FastDiv items;      // of a token
-    uint32_t total;     // of all tokens
+    // An item, a warp's work, is a run of passes over one side (q or k) of a token; first the items of all
+    // tokens' q, then of their k, so that the warps of a block, and the last blocks, have equal ones
+    int per_item[2];    // passes of an item (q, k)
+    FastDiv items[2];   // items of a token
+    uint32_t q_total, total;
     unsigned int *err;
 };
 
@@ -287,13 +288,16 @@ struct HeadItem {
     int head, end, passes;   // this lane's first head, the side's number of heads, passes of the item
     const T *x;              // this lane's elements of that head
     __device__ __forceinline__ HeadItem(const HeadKernelArgs &a, uint32_t item, int sub, bool in_pass, int p0) {
-        const uint32_t token = fdiv(item, a.items), i = item - token * a.items.d;
-        is_k = (int)i >= a.q_items;
+        is_k = item >= a.q_total;
+        if (is_k) item -= a.q_total;
+        const FastDiv items = is_k ? a.items[1] : a.items[0];
+        const int per_item = is_k ? a.per_item[1] : a.per_item[0];
+        const uint32_t token = fdiv(item, items);
         t = token;
         end = is_k ? a.h.k_heads : a.h.q_heads;
-        const int first = (int)(is_k ? i - a.q_items : i) * a.per_item * a.per_pass;
+        const int first = (int)(item - token * items.d) * per_item * a.per_pass;
         const int left = (end - first + a.per_pass - 1) / a.per_pass;
-        passes = left < a.per_item ? left : a.per_item;
+        passes = left < per_item ? left : per_item;
         head = first + sub;
         if (!in_pass) end = 0;   // lanes past the last head have none
         x = (is_k ? (const T *)a.h.k + t * a.h.k_stride : (const T *)a.h.q + t * a.h.q_stride) + (int64_t)head * a.h.head_dim + p0;
@@ -301,9 +305,9 @@ struct HeadItem {
 };
 
 template <typename T, int UNITS, bool IL>
-__global__ void __launch_bounds__(kHeadThreads, UNITS > 0 ? 8 : 7) k_qk_norm_rope(HeadKernelArgs a) {
+__global__ void __launch_bounds__(kHeadThreads, 8) k_qk_norm_rope(HeadKernelArgs a) {
     // passes whose loads are in flight (bf16: 2 take 37 us, 8 43; fp32: 4 64 us)
-    constexpr int kDepth = sizeof(T) == 2 ? 4 : 2;
+    constexpr int kDepth = sizeof(T) == 2 && UNITS > 0 ? 4 : 2;
     const HeadArgs &h = a.h;
     const int lane = threadIdx.x & 31;
     const LanePlace<UNITS, IL> q(a, lane);
@@ -565,15 +569,18 @@ cudaError_t launch_qk_norm_rope(const HeadArgs &h, cudaStream_t s) {
     a.per_pass = 32 / a.units;
     // Few tokens: a token's heads are spread over warps, down to one pass each;
     // many: a warp does up to kHeadPasses passes and reads its angles once.
-    const int64_t qp = (h.q_heads + a.per_pass - 1) / a.per_pass, kp = (h.k_heads + a.per_pass - 1) / a.per_pass;
-    int64_t per = h.tokens * (qp + kp) / ((int64_t)sm_count() * 16);
-    per = per < 1 ? 1 : per > kHeadPasses ? kHeadPasses : per;
-    while (h.tokens * ((qp + per - 1) / per + (kp + per - 1) / per) >= ((int64_t)1 << 31)) per *= 2;   // items are counted in 31 bits (tokens in 30: two items of a token fit)
-    a.per_item = (int)per;
-    a.q_items = (int)((qp + per - 1) / per);
-    const int64_t items = a.q_items + (kp + per - 1) / per;
-    a.items = make_fastdiv((uint32_t)items);
-    a.total = (uint32_t)(h.tokens * items);
+    const int64_t passes[2] = {(h.q_heads + a.per_pass - 1) / a.per_pass, (h.k_heads + a.per_pass - 1) / a.per_pass};
+    int64_t most = h.tokens * (passes[0] + passes[1]) / ((int64_t)sm_count() * 16);
+    most = most < 1 ? 1 : most > kHeadPasses ? kHeadPasses : most;
+    auto items = [&](int side) { return (passes[side] + most - 1) / most; };
+    while (h.tokens * (items(0) + items(1)) >= ((int64_t)1 << 31)) most *= 2;   // items are counted in 31 bits (tokens in 30: two items of a token fit)
+    for (int side = 0; side < 2; side++) {
+        const int64_t n = items(side) ? items(side) : 1;
+        a.per_item[side] = (int)((passes[side] + n - 1) / n);   // equal shares
+        a.items[side] = make_fastdiv((uint32_t)n);
+    }
+    a.q_total = (uint32_t)(h.tokens * items(0));
+    a.total = a.q_total + (uint32_t)(h.tokens * items(1));
     const cudaError_t e = error_word_address(&a.err);
     if (e != cudaSuccess) return e;
     if (h.bf16) return h.interleaved ? pick_units<__nv_bfloat16, true>(a, s) : pick_units<__nv_bfloat16, false>(a, s);
