@@ -33,6 +33,7 @@ struct Groups {
     int off[kMaxGroups + 1];
     int tile[kMaxGroups + 1];   // 128-row scale tiles before each group
     int wide[kMaxGroups + 1];   // blocks of 256 rows before each group
+    int2 sum[kMaxGroups / 32];  // tiles and blocks of 32 groups
 };
 
 // Fills `g` (all threads of the block call this); a table that had to be
@@ -43,33 +44,36 @@ __device__ __forceinline__ void load_groups(Groups &g, const int32_t *offsets, i
         if (offset_wrong(offsets, i, rows)) latch_index_error(err);
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int carry = 0, carry2 = 0;
-        for (int b = 0; b < n; b += 32) {
-            const int e = b + lane;
-            const int rows_e = e < n ? g.off[e + 1] - g.off[e] : 0;
-            const int t = rows_e > 0 ? (rows_e + 127) >> 7 : 0, w = (t + 1) >> 1;
-            int s = t, s2 = w;
+    // a warp scans 32 groups; then each entry adds the sums of the warps before
+    const int lane = threadIdx.x & 31;
+    for (int b = threadIdx.x >> 5; 32 * b < n; b += blockDim.x >> 5) {
+        const int e = 32 * b + lane;
+        const int rows_e = e < n ? g.off[e + 1] - g.off[e] : 0;
+        const int t = rows_e > 0 ? (rows_e + 127) >> 7 : 0, w = (t + 1) >> 1;
+        int s = t, s2 = w;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xFFFFFFFFu, s, o), v2 = __shfl_up_sync(0xFFFFFFFFu, s2, o);
-                if (lane >= o) {
-                    s += v;
-                    s2 += v2;
-                }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, s, o), v2 = __shfl_up_sync(0xFFFFFFFFu, s2, o);
+            if (lane >= o) {
+                s += v;
+                s2 += v2;
             }
-            if (e < n) {
-                g.tile[e] = carry + s - t;
-                g.wide[e] = carry2 + s2 - w;
-            }
-            carry += __shfl_sync(0xFFFFFFFFu, s, 31);
-            carry2 += __shfl_sync(0xFFFFFFFFu, s2, 31);
         }
-        if (lane == 0) {
-            g.tile[n] = carry;
-            g.wide[n] = carry2;
+        if (e < n) {
+            g.tile[e] = s - t;
+            g.wide[e] = s2 - w;
         }
+        if (lane == 31) g.sum[b] = make_int2(s, s2);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e <= n; e += blockDim.x) {
+        int2 before = make_int2(0, 0);
+        for (int b = 0; 32 * b + 31 < e || (e == n && 32 * b < n); b++) {
+            before.x += g.sum[b].x;
+            before.y += g.sum[b].y;
+        }
+        g.tile[e] = before.x + (e < n ? g.tile[e] : 0);
+        g.wide[e] = before.y + (e < n ? g.wide[e] : 0);
     }
     __syncthreads();
 }

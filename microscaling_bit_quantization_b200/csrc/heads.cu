@@ -483,14 +483,14 @@ __global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope_quantize(HeadK
                 }
             } else {
                 amax = group_max<4>(amax);
-                // mx_scale where its result is in the middle of its range: byte eb - emax for the exponent field eb of amax
-                constexpr uint32_t kEmax = F == kMXFP8 ? 8 : 2, kLow = (kEmax + 1) << 23;
-                const uint32_t bits = __float_as_uint(amax);
-                uint32_t sb = (bits >> 23) - kEmax;
+                constexpr int kEmax = F == kMXFP8 ? 8 : 2;
+                uint32_t sb;
+                float inv;
+                const bool mid = mx_scale_mid(amax, kEmax, sb, inv);
                 // (v f) 2^-e rounded once, as v (f 2^-e) where that factor is finite and normal
-                float m = __fmul_rn(f, __uint_as_float((254u - sb) << 23));
-                if (!(bits - kLow <= 0x7F800000u - kLow && m >= 1e-30f && m <= 1e30f)) {   // small, zero or NaN, or far from 1
-                    float inv = 0.0f;
+                float m = __fmul_rn(f, inv);
+                if (!(mid && m >= 1e-30f && m <= 1e30f)) {
+                    inv = 0.0f;
                     const bool zero = !(amax > 0.0f);
                     sb = zero ? 127u : mx_scale(amax, kEmax, inv);
                     m = __fmul_rn(f, inv);

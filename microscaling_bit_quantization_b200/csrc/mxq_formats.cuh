@@ -123,6 +123,16 @@ __device__ __forceinline__ uint32_t mx_scale(float amax, int emax_elem, float &i
     return (uint32_t)(e + 127);
 }
 
+// mx_scale from the exponent field of amax alone, where its byte lies in 1 ..
+// 255 - emax_elem; false elsewhere (amax zero, small or NaN), scale and inv
+// then without meaning.
+__device__ __forceinline__ bool mx_scale_mid(float amax, uint32_t emax_elem, uint32_t &scale, float &inv) {
+    const uint32_t bits = __float_as_uint(amax), low = (emax_elem + 1) << 23;
+    scale = (bits >> 23) - emax_elem;
+    inv = __uint_as_float((254u - scale) << 23);
+    return bits - low <= 0x7F800000u - low;
+}
+
 // MX shared scale with a fixed grid scale g in [1, 2] ("Bridging the Gap
 // ...", MR-GPTQ modification 1: one fixed grid scale for rotated MXFP4): the
 // exponent of g * amax, e = floor(log2 amax) + [g m >= 2] - emax_elem with m
