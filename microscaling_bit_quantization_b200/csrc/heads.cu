@@ -12,15 +12,16 @@
 // both ends of its pairs: 8 consecutive ones when pairs are neighbours
 // (interleaved) or lie behind `rot`, else 4 of the first and the 4 partners of
 // the second half.  A head takes U = D / 8 neighbouring lanes, a warp
-// floor(32 / U) heads at a time (a pass).  A warp's work is an item: up to 8
-// passes over the q heads, or the k heads, of one token, so that a lane's
+// floor(32 / U) heads at a time (a pass).  A warp's work is an item: up to
+// 16 passes over the q heads, or the k heads, of one token, so that a lane's
 // weights and angles, joined to one linear map, serve them all and pointers
-// only step.  Sums run over the U lanes by shuffles: butterflies where U is a
+// only step; the items of all q come before those of all k.  Sums run over the U lanes by shuffles: butterflies where U is a
 // power of two, else a tree.
 // Bound: instruction issue and latency together (8192 tokens x 40 heads x 128
-// in bf16: 41 us, 4.2 TB/s, 137 instructions per pass of 256 elements, 56% of
-// issue slots used; items of 16 passes 48 us, of 4 40 us, of 2 52 us: a long
-// item leaves warps idle at the end, a short one reads its angles again).
+// in bf16: 31 us, 5.4 TB/s, 125 instructions per pass of 256 elements, 67% of
+// issue slots used; items of up to 8 passes 34 us, of 6 35: a short one waits
+// for its angles as long as a long one; a token's q and k items side by side,
+// unequal in a block and at the end, 35 us with 8 passes, 37 with 16).
 #include <cuda_runtime.h>
 
 #include "groups.cuh"
@@ -405,8 +406,10 @@ __device__ __forceinline__ void hadamard_heads(Pairs &v, int b, int lane) {
 // them so; pairs of halves go through shared memory (1 KB per warp), stored so
 // that both 16-byte reads give even and odd elements apart.  The head's factor
 // and 1/sqrt(b) are applied where the codes are formed.  Bound: instruction
-// issue (the same heads to MXFP8: 44 us, with a Hadamard rotation of 128 58 us,
-// half of what it adds being the four exchanges of 8 values across lanes).
+// issue (the same heads to MXFP8: 37 us, with a Hadamard rotation of 128 49 us,
+// 270 instructions per pass and 80% of issue slots used; two passes unrolled
+// 67 us and the cross-lane stages as a loop 63 us where the kernel took 57:
+// the instructions have to fit the fetch and be few).
 template <typename T, int F, int UNITS, bool IL>
 __global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope_quantize(HeadKernelArgs a) {
     __shared__ __align__(16) float buf[IL ? 1 : kHeadWarps][IL ? 4 : 256];
