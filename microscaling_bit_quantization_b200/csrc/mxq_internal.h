@@ -202,7 +202,6 @@ cudaError_t launch_mixed_scatter(const void *const ybuf[3], const int64_t n_grou
 // in 31 bits.
 constexpr int kMaxGroups = 512;
 constexpr int64_t kMaxGroupedRows = (int64_t)1 << 22;
-constexpr int kPlanMaxBlocks = 128;
 // 128-row tiles that the rows of n_groups groups can need: every group begins
 // a tile of its own.
 inline int64_t grouped_scale_tiles(int64_t rows, int64_t n_groups) {
