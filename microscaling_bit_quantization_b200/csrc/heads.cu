@@ -18,7 +18,7 @@
 // only step; the items of all q come before those of all k.  Sums run over the U lanes by shuffles: butterflies where U is a
 // power of two, else a tree.
 // Bound: instruction issue and latency together (8192 tokens x 40 heads x 128
-// in bf16: 31 us, 5.4 TB/s, 125 instructions per pass of 256 elements, 67% of
+// in bf16: 30.5 us, 5.5 TB/s, some 125 instructions per pass of 256 elements, 67% of
 // issue slots used; items of up to 8 passes 34 us, of 6 35: a short one waits
 // for its angles as long as a long one; a token's q and k items side by side,
 // unequal in a block and at the end, 35 us with 8 passes, 37 with 16).
@@ -45,6 +45,9 @@ struct HeadKernelArgs {
     int per_item[2];    // passes of an item (q, k)
     FastDiv items[2];   // items of a token
     uint32_t q_total, total;
+    // 1 / head_dim; for the sum of squares that and eps times the Hadamard size b (exact, a power of two), so that the
+    // head's factor carries 1/sqrt(b)
+    float inv_d, scale, eps;
     unsigned int *err;
 };
 
@@ -222,11 +225,10 @@ __device__ __forceinline__ Turn turn_of(const float *w, int p0, int p1, bool tur
 // before the head's factor r = 1/sqrt(mean square + eps), which is returned
 // (the map is linear: one multiplication less, and none waits for the sum).
 template <int UNITS>
-__device__ __forceinline__ float norm_turn(Pairs &v, const HeadArgs &h, const Turn &t, bool turned, int u, int units, int lane) {
-    const float inv_d = 1.0f / (float)h.head_dim;
-    if (h.norm == 1) {
+__device__ __forceinline__ float norm_turn(Pairs &v, const HeadKernelArgs &k, const Turn &t, bool turned, int u, int lane) {
+    if (k.h.norm == 1) {
         const float2 s2 = __fadd2_rn(__fadd2_rn(v.a[0], v.a[1]), __fadd2_rn(v.b[0], v.b[1]));
-        const float m = -head_sum<UNITS>(s2.x + s2.y, u, units, lane) * inv_d;
+        const float m = -head_sum<UNITS>(s2.x + s2.y, u, k.units, lane) * k.inv_d;
         const float2 mm = make_float2(m, m);
 #pragma unroll
         for (int i = 0; i < 2; i++) {
@@ -235,7 +237,7 @@ __device__ __forceinline__ float norm_turn(Pairs &v, const HeadArgs &h, const Tu
         }
     }
     const float2 q2 = fma2(v.b[1], v.b[1], fma2(v.b[0], v.b[0], fma2(v.a[1], v.a[1], mul2(v.a[0], v.a[0]))));
-    const float r = rsqrtf(fmaf(head_sum<UNITS>(q2.x + q2.y, u, units, lane), inv_d, h.eps));
+    const float r = rsqrtf(fmaf(head_sum<UNITS>(q2.x + q2.y, u, k.units, lane), k.scale, k.eps));
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         float2 a = mul2(t.aa[i], v.a[i]), b = mul2(t.bb[i], v.b[i]);
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(kHeadThreads, 8) k_qk_norm_rope(HeadKernelArgs
                 if (pass + j < in.passes) {
                     Pairs v = unpack<IL>(raw[j]);
                     if (pass + j + kDepth < in.passes) fetch(raw[j]);
-                    float r = norm_turn<UNITS>(v, h, turn, q.turned, q.u, a.units, lane);
+                    float r = norm_turn<UNITS>(v, a, turn, q.turned, q.u, lane);
                     if (pos < 0) r = __int_as_float(0x7FC00000);
                     if (in.head < in.end) {
                         // a lane stores the elements it loaded and no others: q_out = q and k_out = k are allowed
@@ -405,9 +407,9 @@ __device__ __forceinline__ void hadamard_heads(Pairs &v, int b, int lane) {
 // Codes want a lane to hold 8 neighbouring elements.  Interleaved pairs have
 // them so; pairs of halves go through shared memory (1 KB per warp), stored so
 // that both 16-byte reads give even and odd elements apart.  The head's factor
-// and 1/sqrt(b) are applied where the codes are formed.  Bound: instruction
-// issue (the same heads to MXFP8: 37 us, with a Hadamard rotation of 128 49 us,
-// 270 instructions per pass and 80% of issue slots used; two passes unrolled
+// (with 1/sqrt(b) in it) is applied where the codes are formed.  Bound: instruction
+// issue (the same heads to MXFP8: 36 us, with a Hadamard rotation of 128 48 us,
+// some 270 instructions per pass and 80% of issue slots used; two passes unrolled
 // 67 us and the cross-lane stages as a loop 63 us where the kernel took 57:
 // the instructions have to fit the fetch and be few).
 template <typename T, int F, int UNITS, bool IL>
@@ -418,7 +420,6 @@ __global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope_quantize(HeadK
     float *b = buf[IL ? 0 : threadIdx.x >> 5];
     const LanePlace<UNITS, IL> q(a, lane);
     const int d = h.head_dim, step = a.per_pass * d, apart = q.p1 - q.p0;
-    const float norm = h.hadamard_b ? __frsqrt_rn((float)h.hadamard_b) : 1.0f;
     constexpr int kPerByte = F == kMXFP4 ? 2 : 1;
     const int code_step = step / kPerByte, scale_step = a.per_pass * (F == kINT8Row ? 4 : d / 32);
     pdl_wait();
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope_quantize(HeadK
             in.head += a.per_pass;
             in.x += step;
             if (in.head < in.end && pass + 1 < in.passes) load_raw<IL>(raw, in.x, apart);
-            const float f = norm_turn<UNITS>(v, h, turn, q.turned, q.u, a.units, lane) * norm;
+            const float f = norm_turn<UNITS>(v, a, turn, q.turned, q.u, lane);
             if (!IL) {
                 __syncwarp();   // the pass before has been read
                 if (q.in_pass) {
@@ -569,6 +570,10 @@ cudaError_t launch_qk_norm_rope(const HeadArgs &h, cudaStream_t s) {
     HeadKernelArgs a = {};
     a.h = h;
     a.units = h.head_dim / 8;
+    const float b = h.hadamard_b ? (float)h.hadamard_b : 1.0f;
+    a.inv_d = 1.0f / (float)h.head_dim;
+    a.scale = a.inv_d * b;
+    a.eps = h.eps * b;
     a.per_pass = 32 / a.units;
     // Few tokens: a token's heads are spread over warps, down to one pass each;
     // many: a warp does up to kHeadPasses passes and reads its angles once.
