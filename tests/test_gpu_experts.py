@@ -64,6 +64,13 @@ def test_plan(mxq, tokens, topk, n, dtype):
     check_plan(mxq, ids, n, dtype)
 
 
+@pytest.mark.parametrize("rows", [4096, 4098, 5120, 74 * 1024 - 1, 74 * 1024, 74 * 1024 + 1, 74 * 2048 + 1, 300007])
+def test_plan_block_boundaries(mxq, rows):
+    """Sizes at which the number of blocks, or of a block's rounds, changes."""
+    ids = np.random.default_rng(rows).integers(-1, 300, (rows, 1))
+    check_plan(mxq, ids, 300, torch.int64 if rows & 1 else torch.int32)
+
+
 def test_plan_one_expert_none_and_far_ids(mxq):
     check_plan(mxq, np.full((3000, 2), 5), 9, torch.int32)
     check_plan(mxq, np.full((9000, 2), 5), 9, torch.int64)

@@ -216,6 +216,33 @@ def test_empty_zero_rows_and_graph(mxq):
     assert torch.equal(again[0], want[0]) and mxq.check() == 0
 
 
+@pytest.mark.parametrize("fmt", [None, MXFP8, MXFP4, INT8_ROW])
+@pytest.mark.parametrize("tokens,hq,hk,d,interleaved", [(700, 77, 5, 128, True), (700, 77, 5, 128, False), (300, 3, 130, 96, True),
+                                                        (2000, 33, 1, 160, False), (1, 300, 300, 32, True), (129, 16, 17, 256, False)])
+def test_heads_do_not_depend_on_their_neighbours(mxq, fmt, tokens, hq, hk, d, interleaved):
+    """However many heads and tokens share a call, a head gets the bits it gets alone; either side may have no heads."""
+    gen = torch.Generator("cuda").manual_seed(tokens + hq)
+    q, k = (torch.randn(tokens, h, d, device="cuda", generator=gen).bfloat16() for h in (hq, hk))
+    w = torch.rand(d, device="cuda", generator=gen) + 0.5
+    cos, sin = (torch.from_numpy(a).cuda() for a in tables(tokens, d))
+    had = 0 if fmt is None else d & -d
+
+    def f(q, k, lo, hi):
+        pos = torch.arange(lo, hi, device="cuda", dtype=torch.int32)
+        if fmt is None:
+            return [o for o in mxq.qk_norm_rope(q, k, w, w, cos, sin, pos, interleaved=interleaved)]
+        out = mxq.qk_norm_rope_quantize(q, k, w, w, cos, sin, pos, interleaved=interleaved, fmt=fmt, hadamard_b=had)
+        return [mxq.dequantize(o).view(hi - lo, -1, d) if o.rows else None for o in out]
+
+    qa, ka = f(q, k, 0, tokens)
+    for lo, hi, h0, h1, g0, g1 in ((0, tokens, 0, 1, hk - 1, hk), (tokens // 2, tokens // 2 + 1, hq // 2, hq, 0, hk),
+                                   (tokens - 1, tokens, hq - 1, hq, 0, 1), (0, tokens, 0, 0, 0, hk), (0, tokens, 0, hq, 0, 0)):
+        qp, kp = f(q[lo:hi, h0:h1].contiguous(), k[lo:hi, g0:g1].contiguous(), lo, hi)
+        assert h1 == h0 or torch.equal(qp, qa[lo:hi, h0:h1])
+        assert g1 == g0 or torch.equal(kp, ka[lo:hi, g0:g1])
+    assert mxq.check() == 0
+
+
 @pytest.mark.parametrize("fmt", [None, MXFP8])
 def test_tokens_past_32_bits(mxq, fmt):
     """2.5 G elements: the last tokens as a call on them alone gives them."""
