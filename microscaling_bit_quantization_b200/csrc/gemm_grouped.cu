@@ -17,8 +17,9 @@
 //               bytes, the box of 16 / 32 / 64 / 128 rows of X that fits, the
 //               scale atoms of both
 //   warp 1      TMEM allocation and the thread that issues the MMAs
-//   warps 2-5   epilogue, one per TMEM lane quarter
-//   warps 6-    (block-scaled formats) a thread per scale atom of a stage, which
+//   warps 2-5   epilogue, one per TMEM lane quarter (pairs of the formats without
+//               block scales may have a second one for each)
+//   the rest    (block-scaled formats) a thread per scale atom of a stage, which
 //               copies it to TMEM: a tcgen05.cp holds up the thread that issues
 //               it, and NVFP4 has eight a stage (one token, 8 of 64 experts,
 //               2048 x 4096: 15.1 us with the MMA thread issuing them, 12.7 with
@@ -229,14 +230,15 @@ __device__ __forceinline__ void prefetch_maps(const GroupedParams &p, int warp, 
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
 }
-// Whether all 128 epilogue threads say so: they meet at barriers, so they go
+// Whether all epilogue threads of a pair's CTA say so: they meet at barriers, so they go
 // on together or not at all.
+template <int THREADS>
 __device__ __forceinline__ bool all_epilogue(bool ok) {
     int all;
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, 2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\tbar.red.and.pred q, 2, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
         : "=r"(all)
-        : "r"((int)ok)
+        : "r"((int)ok), "n"(THREADS)
         : "memory");
     return all != 0;
 }
@@ -288,6 +290,13 @@ __device__ __forceinline__ Item item_at(const Groups &g, int n_groups, int n_til
 template <int F, int NB>
 struct Pair {
     static constexpr int kAtoms = gg_atoms<F>();
+    // Epilogue warps, kSplit per TMEM lane quarter, which take its chunks in turn.  Two where blocks are tall and no
+    // scales are copied: the last item's epilogue runs under nothing (INT8, 8 experts of 1160 x 4608, 2000 rows: 23.4
+    // us with one, 21.2 with two).  With block scales one: NVFP4, 32 experts of 4096 x 4096, 32,768 rows 323 us, 335
+    // with two.
+    static constexpr int kSplit = NB == 256 && kAtoms == 0 ? 2 : 1;
+    static constexpr int kEpi = 4 * kSplit;
+    static constexpr int kThreads = 32 * (2 + kEpi + kAtoms);
     static constexpr int kXBytes = NB / 2 * 128;
     static constexpr int kSfBytes = 2048 + NB * 16;        // W's atoms, then X's by 128 rows
     static constexpr int kStage = GG_W + kXBytes + kSfBytes;
@@ -327,7 +336,7 @@ __device__ __forceinline__ void tc_cp_pair(uint32_t taddr, uint64_t sdesc) {
 }
 
 template <int F, int NB>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gg_threads<F>(), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<F, NB>::kThreads, 1)
     k_gemm_grouped_pair(const __grid_constant__ GroupedParams p) {
     using P = Pair<F, NB>;
     constexpr int ST = P::kStages;
@@ -359,9 +368,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gg_threads<F>(), 1)
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(accf + i, 1);
-            mbar_init(acce + i, 8);   // 4 epilogue warps x 2 CTAs
+            mbar_init(acce + i, 2 * P::kEpi);   // the epilogue warps of both CTAs
         }
-        mbar_init(ovlf, 8);
+        mbar_init(ovlf, 2 * P::kEpi);
         mbar_init(drain, 1 + NSF);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -458,8 +467,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gg_threads<F>(), 1)
                 mbar_wait(drain, 0, p.wait_ns);
             }
         }
-    } else if (warp >= 6) {
-        const int atom = warp - 6;
+    } else if (warp >= 2 + P::kEpi) {
+        const int atom = warp - 2 - P::kEpi;
         if (NSF && lane == 0 && rank == 0) {
             int it = 0;
             for (int item = cid; item < items && !*abort_flag; item += ncl) {
@@ -493,13 +502,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gg_threads<F>(), 1)
         }
     } else {
         const int q = warp & 3, feature = q * 32 + lane;   // TMEM lane quarter and lane
+        constexpr int SP = P::kSplit;
+        const int part = (warp - 2) >> 2;                  // this warp's chunks: part, part + SP, ..
         const uint32_t ovl_to = map_to_rank(ovlf, 0), acce_to = map_to_rank(acce, 0);   // acce + 1: 8 bytes on
         int count = 0;
         for (int item = cid; item < items; item += ncl, count++) {
             const Item w = item_at<WIDE>(groups, p.n_groups, p.n_tiles, item);
             const int st = count & 1;
             const bool ok = !*abort_flag && mbar_wait(accf + st, (count >> 1) & 1, p.wait_ns);
-            if (!all_epilogue(ok)) {
+            if (!all_epilogue<32 * P::kEpi>(ok)) {
                 if (!ok && !*abort_flag) atomicOr(p.err, kErrGrouped);
                 *abort_flag = 1;
                 break;
@@ -516,35 +527,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gg_threads<F>(), 1)
             constexpr int kShared = P::kShared;
             int first = 0, shared = 0;
             if constexpr (kShared > 0) {
+                constexpr int kOwn = (kShared + SP - 1) / SP;
                 first = st ? 0 : 5;
                 shared = n_chunks - first < 0 ? 0 : n_chunks - first < kShared ? n_chunks - first : kShared;
-                uint32_t ro[kShared][32];
+                uint32_t ro[kOwn][32];
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < kShared; i++)
-                    if (i < shared) tmem_ld_32x32b_x32_async(acc + 32u * (first + i), ro[i]);
-                tmem_ld_wait(ro[kShared - 1]);
+                for (int i = 0; i < kOwn; i++)
+                    if (SP * i + part < shared) tmem_ld_32x32b_x32_async(acc + 32u * (first + SP * i + part), ro[i]);
+                tmem_ld_wait(ro[kOwn - 1]);
 #pragma unroll
-                for (int i = 0; i + 1 < kShared; i++) tmem_reg_tie(ro[i]);
+                for (int i = 0; i + 1 < kOwn; i++) tmem_reg_tie(ro[i]);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote_relaxed(ovl_to);
 #pragma unroll
-                for (int i = 0; i < kShared; i++)
-                    if (i < shared) process(first + i, ro[i]);
+                for (int i = 0; i < kOwn; i++)
+                    if (SP * i + part < shared) process(first + SP * i + part, ro[i]);
             }
             const int others = n_chunks - shared;
-            if (others == 0) {
+            if (part >= others) {   // none for this warp
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote_relaxed(acce_to + 8u * st);
             }
 #pragma unroll 1
-            for (int i = 0; i < others; i++) {
+            for (int i = part; i < others; i += SP) {
                 const int c = st ? shared + i : i;
                 uint32_t r[32];
                 __syncwarp();
                 tmem_ld_32x32b_x32(acc + 32u * c, r);
-                if (i == others - 1) {   // the whole stage is drained
+                if (i + SP >= others) {   // this warp's last
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_relaxed(acce_to + 8u * st);
@@ -803,7 +815,7 @@ cudaError_t launch_pair(const GroupedParams &p, int clusters, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
-    cfg.blockDim = dim3(gg_threads<F>(), 1, 1);
+    cfg.blockDim = dim3(Pair<F, NB>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
