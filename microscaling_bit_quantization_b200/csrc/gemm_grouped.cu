@@ -578,17 +578,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<F, NB>::kThread
 // ---- K split over a cluster
 //
 // A cluster holds one item, 128 features x up to 128 rows; CTA r of S does
-// k-tiles [KT r / S, KT (r + 1) / S) with cta_group::1 MMAs, leaves its sums by
-// chunks of 32 rows in shared memory, and adds its share of a chunk's rows from
-// all CTAs over distributed shared memory in rank order: no atomics, no
-// workspace, the same bits from run to run.  INT8 sums are added as integers.
+// k-tiles [KT r / S, KT (r + 1) / S) with cta_group::1 MMAs, leaves its sums in
+// the shared memory of the ring, which is done with, and adds its share of the
+// rows from all CTAs over distributed shared memory in rank order: no atomics,
+// no workspace, the same bits from run to run.  INT8 sums are added as
+// integers.
 
 constexpr int GS_STAGES = 5;
 constexpr int GS_X = 128 * 128;
 constexpr int GS_SF = 2048;   // up to 4 atoms, for W and for X
 constexpr int GS_STAGE = GG_W + GS_X + 2 * GS_SF;
-constexpr int GS_STAGING = 32 * 128 * 4;
-constexpr int GS_SMEM = GS_STAGES * GS_STAGE + GS_STAGING + (int)sizeof(Groups) + 256 + 1024;
+constexpr int GS_SMEM = GS_STAGES * GS_STAGE + (int)sizeof(Groups) + 256 + 1024;
+static_assert(128 * 128 * 4 <= GS_STAGES * GS_STAGE, "the sums of a block in the ring");
 constexpr uint32_t GS_TMEM_SF = 128;   // the accumulator's 128 columns, then 32 of scales per stage
 static_assert(GS_TMEM_SF + 32 * GS_STAGES <= 512, "TMEM budget");
 static_assert(GS_SMEM <= 227 * 1024, "shared memory budget");
@@ -597,17 +598,16 @@ template <int F>
 __global__ void __launch_bounds__(gg_threads<F>(), 1) k_gemm_grouped_split(const __grid_constant__ GroupedParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    uint32_t *staging = reinterpret_cast<uint32_t *>(smem + GS_STAGES * GS_STAGE);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + GS_STAGES * GS_STAGE + GS_STAGING);
+    uint32_t *sums = reinterpret_cast<uint32_t *>(smem);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + GS_STAGES * GS_STAGE);
     uint64_t *empty = full + GS_STAGES;
     uint64_t *sfready = empty + GS_STAGES;   // [GS_STAGES] a stage's scales in TMEM
     uint64_t *accf = sfready + GS_STAGES;    // the sums are in TMEM
-    uint64_t *ready = accf + 1;              // a chunk of every CTA's sums is in its staging
-    uint64_t *freed = ready + 1;             // and has been read by all of them
-    uint64_t *drain = freed + 1;
+    uint64_t *ready = accf + 1;              // every CTA's sums are in its shared memory
+    uint64_t *drain = ready + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    Groups &groups = *reinterpret_cast<Groups *>(smem + GS_STAGES * GS_STAGE + GS_STAGING + 256);
+    Groups &groups = *reinterpret_cast<Groups *>(smem + GS_STAGES * GS_STAGE + 256);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t split;
@@ -625,7 +625,6 @@ __global__ void __launch_bounds__(gg_threads<F>(), 1) k_gemm_grouped_split(const
         }
         mbar_init(accf, 1);
         mbar_init(ready, 4 * split);
-        mbar_init(freed, 4 * split);
         mbar_init(drain, 1 + NSF);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -727,44 +726,38 @@ __global__ void __launch_bounds__(gg_threads<F>(), 1) k_gemm_grouped_split(const
         } else {
             const int q = warp & 3, feature = q * 32 + lane;   // TMEM lane quarter and lane
             const int et = threadIdx.x - 64, v8 = et & 15;     // 0 .. 127 among the epilogue threads; 8 features to store
-            const int per = 32 / (int)split, n_chunks = (w.n_rows + 31) >> 5;
             const float alpha = scale_of<F>(p, w.group);
             bool ok = mbar_wait(accf, 0, p.wait_ns) && !*abort_flag;
             tc_fence_after();
-            for (int c = 0; c < n_chunks; c++) {
+            for (int c = 0; c < (w.n_rows + 31) >> 5; c++) {
                 uint32_t r[32];
                 __syncwarp();
                 tmem_ld_32x32b_x32(tmem + ((uint32_t)(q * 32) << 16) + 32u * c, r);
-                if (c > 0 && ok) ok = mbar_wait<true>(freed, (c - 1) & 1, p.wait_ns);
 #pragma unroll
-                for (int j = 0; j < 32; j++) staging[j * 128 + feature] = r[j];
-                __syncwarp();
-                if (lane < (int)split) mbar_arrive_remote(map_to_rank(ready, lane));
-                if (ok) ok = mbar_wait<true>(ready, c & 1, p.wait_ns);
-                // rows rank * per .. of the chunk, 8 features per thread
-                for (int j = et >> 4; j < per && ok; j += 8) {
-                    const int jr = (int)rank * per + j;
-                    if (c * 32 + jr >= w.n_rows) break;
-                    float v[8] = {};
-                    int vi[8] = {};
-                    for (uint32_t s = 0; s < split; s++) {
-                        const uint32_t at = map_to_rank(staging + jr * 128 + v8 * 8, s);
-                        const float4 a = ld_cluster_f4(at), b = ld_cluster_f4(at + 16);
-                        const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                for (int j = 0; j < 32; j++) sums[(c * 32 + j) * 128 + feature] = r[j];
+            }
+            __syncwarp();
+            if (lane < (int)split) mbar_arrive_remote(map_to_rank(ready, lane));
+            if (ok) ok = mbar_wait<true>(ready, 0, p.wait_ns);
+            // every split-th eight rows, 8 features per thread
+            for (int j = (int)rank * 8 + (et >> 4); j < w.n_rows && ok; j += 8 * (int)split) {
+                float v[8] = {};
+                int vi[8] = {};
+                for (uint32_t s = 0; s < split; s++) {
+                    const uint32_t at = map_to_rank(sums + j * 128 + v8 * 8, s);
+                    const float4 a = ld_cluster_f4(at), b = ld_cluster_f4(at + 16);
+                    const float u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-                        for (int i = 0; i < 8; i++) {
-                            if (F == kINT8Row) vi[i] += __float_as_int(u[i]);
-                            else v[i] = __fadd_rn(v[i], u[i]);
-                        }
+                    for (int i = 0; i < 8; i++) {
+                        if (F == kINT8Row) vi[i] += __float_as_int(u[i]);
+                        else v[i] = __fadd_rn(v[i], u[i]);
                     }
-                    if (F == kINT8Row) {
-#pragma unroll
-                        for (int i = 0; i < 8; i++) v[i] = (float)vi[i];
-                    }
-                    store_row8<F>(p, v, w.group, w.row0 + c * 32 + jr, w.tile_n * 128 + v8 * 8, alpha);
                 }
-                __syncwarp();
-                if (lane < (int)split) mbar_arrive_remote(map_to_rank(freed, lane));
+                if (F == kINT8Row) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) v[i] = (float)vi[i];
+                }
+                store_row8<F>(p, v, w.group, w.row0 + j, w.tile_n * 128 + v8 * 8, alpha);
             }
             if (!ok) {
                 if (!*abort_flag) atomicOr(p.err, kErrGrouped);
@@ -774,7 +767,7 @@ __global__ void __launch_bounds__(gg_threads<F>(), 1) k_gemm_grouped_split(const
     }
 
     tc_fence_before();
-    cluster_sync();   // no CTA leaves while another may read its staging
+    cluster_sync();   // no CTA leaves while another may read its sums
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
