@@ -17,8 +17,7 @@
 //               bytes, the box of 16 / 32 / 64 / 128 rows of X that fits, the
 //               scale atoms of both
 //   warp 1      TMEM allocation and the thread that issues the MMAs
-//   warps 2-5   epilogue, one per TMEM lane quarter (pairs of the formats without
-//               block scales may have a second one for each)
+//   warps 2-5   epilogue, one per TMEM lane quarter (pairs may have 6-9 too)
 //   the rest    (block-scaled formats) a thread per scale atom of a stage, which
 //               copies it to TMEM: a tcgen05.cp holds up the thread that issues
 //               it, and NVFP4 has eight a stage (one token, 8 of 64 experts,
@@ -230,8 +229,8 @@ __device__ __forceinline__ void prefetch_maps(const GroupedParams &p, int warp, 
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
 }
-// Whether all epilogue threads of a pair's CTA say so: they meet at barriers, so they go
-// on together or not at all.
+// Whether all epilogue threads of a pair's CTA say so: they meet at barriers,
+// so they go on together or not at all.
 template <int THREADS>
 __device__ __forceinline__ bool all_epilogue(bool ok) {
     int all;
@@ -287,15 +286,10 @@ __device__ __forceinline__ Item item_at(const Groups &g, int n_groups, int n_til
 //     with a full block (two of 256 do not fit beside the scales): the epilogue
 //     takes the shared chunks to registers first and releases them; two stages'
 //     scales in TMEM at a time.
-template <int F, int NB>
+template <int F, int NB, int SP>
 struct Pair {
     static constexpr int kAtoms = gg_atoms<F>();
-    // Epilogue warps, kSplit per TMEM lane quarter, which take its chunks in turn.  Two where blocks are tall and no
-    // scales are copied: the last item's epilogue runs under nothing (INT8, 8 experts of 1160 x 4608, 2000 rows: 23.4
-    // us with one, 21.2 with two).  With block scales one: NVFP4, 32 experts of 4096 x 4096, 32,768 rows 323 us, 335
-    // with two.
-    static constexpr int kSplit = NB == 256 && kAtoms == 0 ? 2 : 1;
-    static constexpr int kEpi = 4 * kSplit;
+    static constexpr int kEpi = 4 * SP;   // epilogue warps: SP per TMEM lane quarter, which take its chunks in turn
     static constexpr int kThreads = 32 * (2 + kEpi + kAtoms);
     static constexpr int kXBytes = NB / 2 * 128;
     static constexpr int kSfBytes = 2048 + NB * 16;        // W's atoms, then X's by 128 rows
@@ -335,10 +329,10 @@ __device__ __forceinline__ void tc_cp_pair(uint32_t taddr, uint64_t sdesc) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
-template <int F, int NB>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<F, NB>::kThreads, 1)
+template <int F, int NB, int SP>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<F, NB, SP>::kThreads, 1)
     k_gemm_grouped_pair(const __grid_constant__ GroupedParams p) {
-    using P = Pair<F, NB>;
+    using P = Pair<F, NB, SP>;
     constexpr int ST = P::kStages;
     constexpr bool WIDE = NB == 256;
     extern __shared__ uint8_t smem_raw[];
@@ -502,7 +496,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<F, NB>::kThread
         }
     } else {
         const int q = warp & 3, feature = q * 32 + lane;   // TMEM lane quarter and lane
-        constexpr int SP = P::kSplit;
         const int part = (warp - 2) >> 2;                  // this warp's chunks: part, part + SP, ..
         const uint32_t ovl_to = map_to_rank(ovlf, 0), acce_to = map_to_rank(acce, 0);   // acce + 1: 8 bytes on
         int count = 0;
@@ -798,23 +791,23 @@ cudaError_t launch_split(const GroupedParams &p, int clusters, int split, cudaSt
     return cudaLaunchKernelEx(&cfg, k_gemm_grouped_split<F>, p);
 }
 
-template <int F, int NB>
+template <int F, int NB, int SP>
 cudaError_t launch_pair(const GroupedParams &p, int clusters, cudaStream_t s) {
-    constexpr int smem = Pair<F, NB>::kSmem;
+    constexpr int smem = Pair<F, NB, SP>::kSmem;
     static PerDeviceOnce smem_opt_in;
     cudaError_t e = smem_opt_in.run([] {
-        return cudaFuncSetAttribute(k_gemm_grouped_pair<F, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return cudaFuncSetAttribute(k_gemm_grouped_pair<F, NB, SP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
-    cfg.blockDim = dim3(Pair<F, NB>::kThreads, 1, 1);
+    cfg.blockDim = dim3(Pair<F, NB, SP>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1] = {pdl_attribute()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_gemm_grouped_pair<F, NB>, p);
+    return cudaLaunchKernelEx(&cfg, k_gemm_grouped_pair<F, NB, SP>, p);
 }
 
 // The host knows the rows of all experts together, not of each; blocks: what
@@ -826,6 +819,12 @@ cudaError_t launch_pair(const GroupedParams &p, int clusters, cudaStream_t s) {
 //   Else pairs; blocks of 128 rows up to a mean of 80 rows per expert, of 256
 //   above (8 experts of 4096 x 4096, MXFP8: mean 64 30.8 against 33.9 us, mean
 //   128 42.6 against 36.0).
+//   Blocks of 256 rows get two epilogue warps per TMEM lane quarter where the
+//   epilogue shows, in two rounds of items at most or with fewer than eight k-tiles (8
+//   experts of 1160 x 4608, 2000 rows: NVFP4 17.3 us with one, 16.5 with two; 32
+//   of 4096 x 512, 32,768 rows 132 and 109), and always in INT8 and FP8 (the
+//   2000 rows in INT8 23.4 and 21.2).  Else one: with block scales two more
+//   cost (32 of 4096 x 4096, 32,768 rows, NVFP4 323 us with one, 335 with two).
 constexpr int kMaxSplit = 4;
 template <int F>
 cudaError_t launch_fmt(GroupedParams &p, const GroupedOperands &op, cudaStream_t s) {
@@ -842,7 +841,9 @@ cudaError_t launch_fmt(GroupedParams &p, const GroupedOperands &op, cudaStream_t
     if (wide) p.max_tiles = (int)(op.rows / 256 + ragged);
     items = (int64_t)p.max_tiles * p.n_tiles;
     const int clusters = (int)(items < sms / 2 ? items : sms / 2);
-    return wide ? launch_pair<F, 256>(p, clusters, s) : launch_pair<F, 128>(p, clusters, s);
+    if (!wide) return launch_pair<F, 128, 1>(p, clusters, s);
+    if (gg_atoms<F>() == 0 || items <= 2 * clusters || p.num_k_tiles < 8) return launch_pair<F, 256, 2>(p, clusters, s);
+    return launch_pair<F, 256, gg_atoms<F>() ? 1 : 2>(p, clusters, s);
 }
 
 }  // namespace
