@@ -275,6 +275,14 @@ def test_product(mxq, orc, fmt, counts, n, k):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+def test_product_many_rounds_and_k_tiles(mxq, orc, fmt):
+    """Several items per pair of SMs with eight k-tiles and more, blocks of 1 to 256 rows."""
+    ex = Experts(mxq, orc, fmt, [600, 513, 256, 700, 257], 2816, 2048, extra=3)
+    ex.check(mxq, torch.float32)
+    ex.check(mxq, torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("counts", [[3, 0, 140], [700, 5, 600]])
 def test_product_odd_columns_and_8bit_short_k(mxq, orc, fmt, counts):
     """Rows of y that start at no 16-byte boundary, and one k-step of 32 bytes."""
