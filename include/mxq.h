@@ -772,8 +772,10 @@ typedef struct mxq_heads {
  *   products of an element and its weight, beyond 3.4e38 overflow).
  *   q_out, k_out: device, dtype of h, strides in elements as q and k; q_out
  *     may be q (same stride), k_out may be k.
- * A position outside [0, n_positions) makes its token's heads NaN and is
- * reported by mxq_check() as MXQ_EINVAL.
+ * A head with a NaN is NaN; one with an infinite element is NaN there and at
+ * its pair's other end and zero elsewhere (MXQ_NORM_LAYER: NaN).  A position outside
+ * [0, n_positions) makes its token's heads NaN and is reported by mxq_check()
+ * as MXQ_EINVAL.
  * Errors: MXQ_EINVAL (shapes, strides, pointers, alignment), MXQ_ECUDA. */
 mxq_status mxq_qk_norm_rope(const mxq_heads *h, void *q_out, int64_t q_out_stride, void *k_out,
                             int64_t k_out_stride, void *stream);
@@ -782,7 +784,8 @@ mxq_status mxq_qk_norm_rope(const mxq_heads *h, void *q_out, int64_t q_out_strid
  * none; a power of two dividing head_dim) and quantization of the fp32
  * values, for a low-bit cache or product: codes and scales in the canonical
  * layout of mxq_quantize, of a (tokens * heads) x head_dim matrix (row
- * t * heads + head), which mxq_dequantize reads.
+ * t * heads + head), which mxq_dequantize reads.  A block (INT8_ROW: a head)
+ * with a NaN among those values gets the NaN scale and reads back as NaN.
  *   fmt: MXQ_MXFP8, MXQ_MXFP4 or MXQ_INT8_ROW (one scale per head); others
  *     MXQ_EUNSUPPORTED.
  * Constraints: head_dim % 32 == 0.  Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED,

@@ -251,6 +251,20 @@ __device__ __forceinline__ float norm_turn(Pairs &v, const HeadKernelArgs &k, co
     return r;
 }
 
+// The larger of two magnitudes, NaN if either is one (fmaxf drops a NaN).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// Over aligned groups of G lanes (G a power of two).
+template <int G>
+__device__ __forceinline__ float group_max_nan(float a) {
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    return a;
+}
+
 // The position of token t, or -1 (reported) for one outside the tables.
 __device__ __forceinline__ int64_t position_of(const HeadArgs &h, int64_t t, unsigned int *err) {
     if (h.rot == 0) return 0;
@@ -441,7 +455,8 @@ __global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope_quantize(HeadK
             in.head += a.per_pass;
             in.x += step;
             if (in.head < in.end && pass + 1 < in.passes) load_raw<IL>(raw, in.x, apart);
-            const float f = norm_turn<UNITS>(v, a, turn, q.turned, q.u, lane);
+            float f = norm_turn<UNITS>(v, a, turn, q.turned, q.u, lane);
+            if (pos < 0) f = __int_as_float(0x7FC00000);
             if (!IL) {
                 __syncwarp();   // the pass before has been read
                 if (q.in_pass) {
@@ -459,34 +474,33 @@ __global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope_quantize(HeadK
                 }
             }
             if (h.hadamard_b) hadamard_heads<UNITS>(v, h.hadamard_b, lane);
-            float amax = fmaxf(fmaxf(fmaxf(fabsf(v.a[0].x), fabsf(v.a[0].y)), fmaxf(fabsf(v.a[1].x), fabsf(v.a[1].y))),
-                               fmaxf(fmaxf(fabsf(v.b[0].x), fabsf(v.b[0].y)), fmaxf(fabsf(v.b[1].x), fabsf(v.b[1].y))));
-            // the largest |v f| is the largest |v| times f: rounding keeps the order
+            float amax = max_nan(max_nan(max_nan(fabsf(v.a[0].x), fabsf(v.a[0].y)), max_nan(fabsf(v.a[1].x), fabsf(v.a[1].y))),
+                                 max_nan(max_nan(fabsf(v.b[0].x), fabsf(v.b[0].y)), max_nan(fabsf(v.b[1].x), fabsf(v.b[1].y))));
+            // the largest |v f| is the largest |v| times f: rounding keeps the order, and a NaN anywhere stays one
+            // (as an infinite v does where the mean square is infinite, f zero)
             amax = __fmul_rn(amax, f);
             if (F == kINT8Row) {
                 if (UNITS) {
-                    amax = group_max<(UNITS ? UNITS : 1)>(amax);
+                    amax = group_max_nan<(UNITS ? UNITS : 1)>(amax);
                 } else {
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) {
                         const float y = __shfl_down_sync(0xFFFFFFFFu, amax, o);
-                        if (q.u < o && q.u + o < a.units) amax = fmaxf(amax, y);
+                        if (q.u < o && q.u + o < a.units) amax = max_nan(amax, y);
                     }
                     amax = __shfl_sync(0xFFFFFFFFu, amax, lane - q.u);
                 }
-                const float s = pos < 0 ? __int_as_float(0x7FC00000) : __fdiv_rn(amax, 127.0f);
+                const float s = __fdiv_rn(amax, 127.0f);
                 const Recip rs = recip_of(s);
                 if (valid) {
                     const float2 ff = make_float2(f, f);
                     const float2 a0 = mul2(v.a[0], ff), a1 = mul2(v.a[1], ff), b0 = mul2(v.b[0], ff), b1 = mul2(v.b[1], ff);
                     const float x[8] = {a0.x, b0.x, a0.y, b0.y, a1.x, b1.x, a1.y, b1.y};
-                    uint2 w = make_uint2(int_x4_quot(x, rs, 127), int_x4_quot(x + 4, rs, 127));
-                    if (pos < 0) w = make_uint2(0x01010101u, 0x01010101u);   // 1 x NaN
-                    *reinterpret_cast<uint2 *>(codes) = w;
+                    *reinterpret_cast<uint2 *>(codes) = make_uint2(int_x4_quot(x, rs, 127), int_x4_quot(x + 4, rs, 127));
                     if (q.u == 0) *reinterpret_cast<float *>(scales) = s;
                 }
             } else {
-                amax = group_max<4>(amax);
+                amax = group_max_nan<4>(amax);
                 constexpr int kEmax = F == kMXFP8 ? 8 : 2;
                 uint32_t sb;
                 float inv;
@@ -496,7 +510,7 @@ __global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope_quantize(HeadK
                 if (!(mid && m >= 1e-30f && m <= 1e30f)) {
                     inv = 0.0f;
                     const bool zero = !(amax > 0.0f);
-                    sb = zero ? 127u : mx_scale(amax, kEmax, inv);
+                    sb = amax != amax ? 255u : zero ? 127u : mx_scale(amax, kEmax, inv);   // 255: the NaN scale
                     m = __fmul_rn(f, inv);
                     if (zero) {
                         v = Pairs{};
@@ -511,7 +525,6 @@ __global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope_quantize(HeadK
                         }
                     }
                 }
-                if (pos < 0) sb = 255u;   // the NaN scale
                 if (valid) {
                     const float2 mm = make_float2(m, m);
                     const float2 a0 = mul2(v.a[0], mm), a1 = mul2(v.a[1], mm), b0 = mul2(v.b[0], mm), b1 = mul2(v.b[1], mm);

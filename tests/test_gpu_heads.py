@@ -261,3 +261,72 @@ def test_tokens_past_32_bits(mxq, fmt):
             assert torch.equal(b[-5:], s)
         else:
             assert torch.equal(b.codes[-5 * h * d:], s.codes) and torch.equal(b.scales[-5 * h * d // 32:], s.scales)
+
+
+@pytest.mark.parametrize("fmt", [MXFP8, MXFP4, INT8_ROW])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot,had", [(64, 64, 0), (96, 64, 0), (96, 64, 32), (128, 96, 0), (128, 128, 128), (256, 256, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+def test_codes_keep_nan(mxq, fmt, interleaved, d, rot, had, dtype, norm):
+    """A block (a head in INT8) with a NaN among its fp32 values reads back as NaN, whatever brought it there; every other
+    block has the codes it has without it."""
+    g = torch.Generator().manual_seed(d + had)
+    q, k = torch.randn(40, 5, d, generator=g), torch.randn(40, 3, d, generator=g)
+    nan, inf = float("nan"), float("inf")
+    clean = [q.clone(), k.clone()]
+    for x, z in zip((q, k), clean):
+        for (t, h, i), v in {(0, 0, 5): nan, (1, 1, d - 1): nan, (7, 2, 0): inf, (8, 0, d - 3): -inf, (9, 1, 33): inf}.items():
+            x[t, h, i] = v
+            z[t, h] = 0
+        x[20, 1] = nan
+        z[20, 1] = 0
+        x[21, 2, 3], x[21, 2, 40] = inf, -inf
+        z[21, 2] = 0
+        x[22, 0], z[22, 0] = x[22, 0] * 1e30, 0           # finite, its squares beyond the largest fp32 value: zeros
+    q, k, *clean = (dev(x.numpy(), dtype) for x in (q, k, *clean))
+    touched = [~torch.isfinite(x).all(2) | (x.abs().amax(2) > 1e20) for x in (q, k)]
+    w = (torch.rand(d, generator=g) + 0.5).cuda()
+    cos, sin = (torch.from_numpy(a).cuda() for a in tables(40, rot))
+
+    def coded(q, k, w, eps=1e-6):
+        return mxq.qk_norm_rope_quantize(q, k, w, w, cos, sin, fmt=fmt, hadamard_b=had, norm=norm, interleaved=interleaved, eps=eps)
+
+    def nans(q, k, w, eps=1e-6):
+        """Blocks of the fp32 outputs, after the rotation, that hold a NaN."""
+        out = []
+        for p in mxq.qk_norm_rope(q.float(), k.float(), w, w, cos, sin, norm=norm, interleaved=interleaved, eps=eps):
+            bad = torch.isnan(p).flatten(0, 1)
+            if had:
+                bad = bad.unflatten(1, (-1, had)).any(2, keepdim=True).expand(-1, -1, had).flatten(1)
+            out.append(bad.unflatten(1, (1 if fmt == INT8_ROW else d // 32, -1)).any(2))
+        return out
+
+    def check(got, bad):
+        for o, b in zip(got, bad):
+            v = mxq.dequantize(o).view(b.shape[0], b.shape[1], -1)
+            assert torch.equal(torch.isnan(v).all(2), b) and torch.equal(torch.isnan(v).any(2), b)
+
+    got, base, bad = coded(q, k, w), coded(*clean, w), nans(q, k, w)
+    check(got, bad)
+    for o, c, b, hit in zip(got, base, bad, touched):
+        assert b.any(1).sum() >= 7 and not b[~hit.flatten()].any()
+        rows = ~hit.flatten()
+        both = lambda z: (z.codes.view(rows.numel(), -1)[rows], z.scales.view(rows.numel(), -1)[rows])  # noqa: E731
+        assert all(torch.equal(m, n) for m, n in zip(both(o), both(c)))
+    if not had:   # and the blocks beside a NaN in its head: what mxq_quantize gives the fp32 outputs
+        for o, p, b in zip(got, mxq.qk_norm_rope(q.float(), k.float(), w, w, cos, sin, norm=norm, interleaved=interleaved), bad):
+            want = mxq.quantize(p.flatten(0, 1), fmt)
+            v, u = (mxq.dequantize(z).view(b.shape[0], b.shape[1], -1)[~b] for z in (o, want))
+            assert torch.equal(v, u)
+    # no mean square at all: zeros with eps 0
+    q[3, 1] = 0
+    bad = nans(q, k, w, 0.0)
+    assert bad[0].view(40, 5, -1)[3, 1].all()
+    check(coded(q, k, w, 0.0), bad)
+    # a weight that is no number
+    w[d - 2] = nan
+    bad = nans(q, k, w)
+    assert all(b.any(1).all() for b in bad)
+    check(coded(q, k, w), bad)
+    assert mxq.check() == 0
