@@ -458,7 +458,8 @@ mxq_status mxq_lowrank_pack_l2(const void *l2, int32_t r, int64_t n, void *l2p, 
  *     (n rows).  The branch is supported for every fmt but INT8_ROW.
  *   y: m x n device, fp32 or bf16 (fp32 result rounded once, RNE).
  * Constraints: K % 64 == 0 (NVFP4, MXFP4), K % g == 0 (INT4_Gg) or
- * K % 32 == 0 (8-bit); K > 0; ceil(m/128) * ceil(n/128) * K/16 < 2^31;
+ * K % 32 == 0 (8-bit); K > 0; K <= 133,144 for INT8_ROW (no sum of products
+ * of its codes then leaves int32); ceil(m/128) * ceil(n/128) * K/16 < 2^31;
  * device pointers 16-byte aligned.
  * Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED (format pair / branch), MXQ_ECUDA.
  * A pipeline wait that runs out is reported by mxq_check(). */
@@ -718,9 +719,10 @@ mxq_status mxq_expert_weight_prepare(const void *w, int32_t wdtype, int32_t hada
  *     fmt and cols those of w.
  *   offsets: device int32[w->n_experts + 1], those xq was written with.
  *   y: xq->rows x w->rows device, fp32 or bf16, 16-byte aligned.
- * Constraints: K % 64 == 0 (4 bits) or K % 32 == 0 (8 bits); pointers 16-byte
- * aligned.  Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED (format, format pair),
- * MXQ_ECUDA; a pipeline wait that runs out is reported by mxq_check(). */
+ * Constraints: K % 64 == 0 (4 bits) or K % 32 == 0 (8 bits); K <= 133,144 for
+ * INT8_ROW; pointers 16-byte aligned.  Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED
+ * (format, format pair), MXQ_ECUDA; a pipeline wait that runs out is reported
+ * by mxq_check(). */
 mxq_status mxq_qlinear_grouped(const mxq_qtensor *xq, const int32_t *offsets, const mxq_expert_weight *w,
                                void *y, int32_t ydtype, void *stream);
 

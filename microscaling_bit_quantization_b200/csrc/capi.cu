@@ -36,6 +36,11 @@ bool valid_shape(int32_t fmt, int64_t rows, int64_t cols) {
     return true;
 }
 
+// Products of INT8_ROW codes (127 in magnitude at most) are added in int32:
+// 127 * 127 * K stays below 2^31.
+constexpr int64_t kMaxInt8Cols = 0x7FFFFFFF / (127 * 127);   // 133,144
+bool int8_sum_fits(int32_t fmt, int64_t k) { return fmt != MXQ_INT8_ROW || k <= kMaxInt8Cols; }
+
 // The last CUDA error a call of this host thread returned as MXQ_ECUDA.
 thread_local cudaError_t g_last_cuda = cudaSuccess;
 mxq_status from_cuda(cudaError_t e) {
@@ -457,7 +462,7 @@ mxq_status mxq_qlinear(const mxq_qtensor *xq, const mxq_qtensor *wq, const void 
     if (xq->layout != MXQ_LAYOUT_MMA || wq->layout != MXQ_LAYOUT_MMA) return MXQ_EINVAL;
     const int64_t m = xq->rows, n = wq->rows, k = xq->cols;
     if (wq->cols != k || k <= 0 || m < 0 || n < 0) return MXQ_EINVAL;
-    if (k % (igroup ? fmt_block(fmt) : fmt_is4(fmt) ? 64 : 32)) return MXQ_EINVAL;
+    if (k % (igroup ? fmt_block(fmt) : fmt_is4(fmt) ? 64 : 32) || !int8_sum_fits(fmt, k)) return MXQ_EINVAL;
     if (!valid_shape(fmt, m, k) || !valid_shape(fmt, n, k)) return MXQ_EINVAL;
     // the kernels count output tiles and their K stages in 32-bit integers
     if (((m + 127) / 128) * ((n + 127) / 128) * (k / 16) >= ((int64_t)1 << 31)) return MXQ_EINVAL;
@@ -933,7 +938,8 @@ mxq_status mxq_expert_weight_bytes(int32_t fmt, int32_t n_experts, int64_t rows,
 static mxq_status check_expert_weight(const mxq_expert_weight *w) {
     if (!w || !valid_fmt(w->fmt) || w->n_experts < 1 || w->n_experts > kMaxGroups) return MXQ_EINVAL;
     if (!grouped_fmt(w->fmt)) return MXQ_EUNSUPPORTED;
-    if (w->rows < 0 || w->cols <= 0 || w->cols % (fmt_is4(w->fmt) ? 64 : 32) || !valid_shape(w->fmt, w->rows, w->cols))
+    if (w->rows < 0 || w->cols <= 0 || w->cols % (fmt_is4(w->fmt) ? 64 : 32) || !int8_sum_fits(w->fmt, w->cols) ||
+        !valid_shape(w->fmt, w->rows, w->cols))
         return MXQ_EINVAL;
     // the kernels index the experts' rows and scale atoms together in 31 bits
     const int64_t tiles = (w->rows + 127) / 128;

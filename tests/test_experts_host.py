@@ -203,3 +203,25 @@ def test_alloc_refuses_no_groups(mxq):
     for n in (0, -1, 513):
         with pytest.raises(mxq.MxqError):
             mxq.alloc_grouped(mxq.MXFP8, 4, n, 64, device="cpu")
+
+
+def test_int8_sums_that_could_leave_int32_are_refused(mxq):
+    """127 * 127 * K < 2^31 up to K = 133,144: the product of two codes' rows cannot wrap in a call that is accepted."""
+    M, L = mxq, mxq.lib()
+    most = (2 ** 31 - 1) // 127 ** 2
+    assert most == 133144
+    good, bad = most // 32 * 32, most // 32 * 32 + 32
+
+    def dense(fmt, k, m=0):
+        a, b = M._QTensorC(fmt, M.MMA, m, k, D, D, D), M._QTensorC(fmt, M.MMA, 4, k, D, D, D)
+        return L.mxq_qlinear(ctypes.byref(a), ctypes.byref(b), None, None, D, 1, None)
+
+    def grouped(fmt, k, m=0):
+        q = M._QTensorC(fmt, M.MMA, m, k, D, D, D)
+        return L.mxq_qlinear_grouped(ctypes.byref(q), D, ctypes.byref(weight(M, fmt=fmt, cols=k)), D, 1, None)
+
+    for f in (dense, grouped):
+        assert f(M.INT8_ROW, good) == 0               # (no rows: nothing to do)
+        assert f(M.INT8_ROW, bad) == EINVAL and f(M.INT8_ROW, bad, 8) == EINVAL
+        assert f(M.FP8_TENSOR, bad) == 0
+    assert L.mxq_expert_weight_prepare(D, 1, 0, ctypes.byref(weight(M, fmt=M.INT8_ROW, cols=bad)), None, 0, None) == EINVAL
