@@ -720,9 +720,9 @@ mxq_status mxq_expert_weight_prepare(const void *w, int32_t wdtype, int32_t hada
  *   offsets: device int32[w->n_experts + 1], those xq was written with.
  *   y: xq->rows x w->rows device, fp32 or bf16, 16-byte aligned.
  * Constraints: K % 64 == 0 (4 bits) or K % 32 == 0 (8 bits); K <= 133,144 for
- * INT8_ROW; pointers 16-byte aligned.  Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED
- * (format, format pair), MXQ_ECUDA; a pipeline wait that runs out is reported
- * by mxq_check(). */
+ * INT8_ROW; pointers 16-byte aligned, fp32 scales, tensor scales and offsets
+ * 4-byte aligned.  Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED (format, format pair),
+ * MXQ_ECUDA; a pipeline wait that runs out is reported by mxq_check(). */
 mxq_status mxq_qlinear_grouped(const mxq_qtensor *xq, const int32_t *offsets, const mxq_expert_weight *w,
                                void *y, int32_t ydtype, void *stream);
 

@@ -862,6 +862,11 @@ bool valid_grouped_scales(int32_t fmt, int64_t rows, int32_t n_groups, int64_t c
     return grouped_scale_tiles(rows, n_groups) * (round_up(cols / fmt_block(fmt), 16) / 4) < ((int64_t)1 << 25);
 }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// Scales of a grouped product's operand: byte scales come by TMA, INT8_ROW's fp32 ones one at a time.
+bool grouped_scales_ok(int32_t fmt, const void *scales) {
+    if (fmt == MXQ_FP8_TENSOR) return true;
+    return scales && (fmt == MXQ_INT8_ROW ? aligned4(scales) : aligned16(scales));
+}
 
 }  // namespace
 
@@ -948,7 +953,7 @@ static mxq_status check_expert_weight(const mxq_expert_weight *w) {
         return MXQ_EINVAL;
     if (w->rows > 0) {
         if (!w->codes || !aligned16(w->codes)) return MXQ_EINVAL;
-        if (w->fmt != MXQ_FP8_TENSOR && (!w->scales || !aligned16(w->scales))) return MXQ_EINVAL;
+        if (!grouped_scales_ok(w->fmt, w->scales)) return MXQ_EINVAL;
         if (fmt_tensor_scaled(w->fmt) && (!w->tensor_scales || !aligned4(w->tensor_scales))) return MXQ_EINVAL;
     }
     return MXQ_OK;
@@ -991,7 +996,7 @@ mxq_status mxq_qlinear_grouped(const mxq_qtensor *xq, const int32_t *offsets, co
         return MXQ_EINVAL;
     if (m == 0 || n == 0) return MXQ_OK;
     if (!y || !aligned16(y) || !xq->codes || !aligned16(xq->codes)) return MXQ_EINVAL;
-    if (xq->fmt != MXQ_FP8_TENSOR && (!xq->scales || !aligned16(xq->scales))) return MXQ_EINVAL;
+    if (!grouped_scales_ok(xq->fmt, xq->scales)) return MXQ_EINVAL;
     if (fmt_tensor_scaled(xq->fmt) && (!xq->tensor_scale || !aligned4(xq->tensor_scale))) return MXQ_EINVAL;
     GroupedOperands op;
     memset(&op, 0, sizeof(op));

@@ -334,6 +334,27 @@ def test_product_same_bits_twice_and_by_parts(mxq, orc, fmt, counts):
     assert (z[:lo] == 3.0).all() and (z[hi:] == 3.0).all()
 
 
+@pytest.mark.parametrize("counts,n,k", [([3, 5, 0, 2], 131, 1152), ([200, 130, 5, 301], 78, 96), ([40, 0, 300, 257], 131, 192)])
+def test_int8_part_of_the_experts_in_place(mxq, orc, counts, n, k):
+    """INT8 scales are fp32, one per channel: the weight of the experts from `first` on is passed as it lies behind the
+    others, wherever its scales begin, and the rows' scales may begin at any fp32 as well."""
+    ex = Experts(mxq, orc, INT8_ROW, counts, n, k, extra=2)
+    y = ex.run(mxq, torch.float32)
+    for first, last in ((1, 4), (2, 4), (3, 4), (0, 2)):
+        part = mxq.ExpertWeight(INT8_ROW, last - first, n, k, ex.w.codes[first * n * k:last * n * k],
+                                ex.w.scales[first * n * 4:last * n * 4], None)
+        room = torch.zeros(ex.xq.scales.numel() + 16, dtype=torch.uint8, device="cuda")
+        at = 4 * first
+        room[at:at + ex.xq.scales.numel()] = ex.xq.scales
+        q = mxq.QTensor(INT8_ROW, mxq.MMA, ex.xq.rows, k, ex.xq.codes, room[at:at + ex.xq.scales.numel()], None)
+        z = torch.full_like(y, 3.0)
+        mxq.qlinear_grouped(q, part, ex.offsets[first:last + 1], out=z)
+        assert mxq.check() == 0
+        lo, hi = int(ex.off[first]), int(ex.off[last])
+        assert torch.equal(z[lo:hi], y[lo:hi])
+        assert (z[:lo] == 3.0).all() and (z[hi:] == 3.0).all()
+
+
 @pytest.mark.parametrize("bad", [[0, 5, 3, 20], [-7, 2, 2, 20], [0, 4, 90, 20], [19, 4, 4, 4], [2 ** 31 - 1] * 4])
 @pytest.mark.parametrize("fmt", [MXFP8, INT8_ROW])
 @pytest.mark.parametrize("scale", [1, 40])
