@@ -733,7 +733,8 @@ mxq_status mxq_qlinear_grouped(const mxq_qtensor *xq, const int32_t *offsets, co
  *     device fp32[tokens][topk] or NULL (all 1).
  *   out: tokens x n fp32/bf16 device, not overlapping y.
  * A slot at or above rows is left out and reported by mxq_check() as
- * MXQ_EINVAL.  Constraints: tokens * n < 2^31.
+ * MXQ_EINVAL.  Constraints: tokens * n < 2^31 (more: a part of the tokens per
+ * call, with its slots, weights and outputs).
  * Errors: MXQ_EINVAL, MXQ_ECUDA. */
 mxq_status mxq_expert_combine(const void *y, int32_t ydtype, int64_t rows, int64_t n, const int32_t *slot,
                               const float *weights, int64_t tokens, int32_t topk, void *out, int32_t odtype,

@@ -891,11 +891,14 @@ def expert_combine(y: torch.Tensor, slot: torch.Tensor, weights: torch.Tensor = 
     tokens, topk = slot.shape
     if out is None:
         out = torch.empty(tokens, n, dtype=out_dtype or y.dtype, device=y.device)
-    _ok(_lib.mxq_expert_combine(_want(y, "y", y.dtype, index), _dtype_code(y), rows, n,
-                                _want(slot, "slot", torch.int32, index),
-                                _want(weights, "weights", torch.float32, index, (tokens, topk)), tokens, topk,
-                                _want(out, "out", out.dtype, index, (tokens, n)), _dtype_code(out), _stream_handle(index)),
-        "mxq_expert_combine")
+    ya, sa, wa = _want(y, "y", y.dtype, index), _want(slot, "slot", torch.int32, index), _want(
+        weights, "weights", torch.float32, index, (tokens, topk))
+    oa = _want(out, "out", out.dtype, index, (tokens, n))
+    most = max(0x7FFFFFFF // max(n, 1), 1)   # tokens of one call: it counts its outputs in 31 bits
+    for t in range(0, max(tokens, 1), most):
+        _ok(_lib.mxq_expert_combine(ya, _dtype_code(y), rows, n, sa + 4 * t * topk, wa and wa + 4 * t * topk,
+                                    min(tokens - t, most), topk, oa + t * n * out.element_size(), _dtype_code(out),
+                                    _stream_handle(index)), "mxq_expert_combine")
     return out
 
 

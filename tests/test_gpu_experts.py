@@ -404,6 +404,26 @@ def test_combine_slots_outside_are_left_out_and_reported(mxq):
     assert (mxq.expert_combine(y[:0], torch.full((2, 3), -1, dtype=torch.int32, device="cuda")) == 0).all()
 
 
+def test_combine_of_more_outputs_than_31_bits_count(mxq):
+    """600,000 tokens of 4096: every token, weights that are powers of two and so exact."""
+    t, n = 600000, 4096
+    g = torch.Generator("cuda").manual_seed(3)
+    y = torch.randn(8, n, device="cuda", generator=g).bfloat16()
+    slot = torch.randint(-1, 8, (t, 1), device="cuda", dtype=torch.int32, generator=g)
+    weights = 2.0 ** torch.randint(-1, 2, (t, 1), device="cuda", generator=g).float()
+    for w in (weights, None):
+        out = mxq.expert_combine(y, slot, w)
+        assert mxq.check() == 0
+        for lo in range(0, t, 100000):
+            s = slot[lo:lo + 100000, 0].long()
+            want = torch.where(s[:, None] >= 0, y[s.clamp(min=0)], torch.zeros_like(y[:1]))
+            assert torch.equal(out[lo:lo + 100000], want if w is None else want * w[lo:lo + 100000].bfloat16())
+    for n in (0, 1):
+        assert (mxq.expert_combine(torch.ones(3, n, device="cuda"), slot[:4].clamp(0, 2)) == 1).all()
+        assert mxq.expert_combine(torch.ones(3, n, device="cuda"), slot[:0]).shape == (0, n)
+    assert mxq.check() == 0
+
+
 # ------------------------------------------------------------------ together
 
 def layer(mxq, x, ids, weights, w, fmt, n):
