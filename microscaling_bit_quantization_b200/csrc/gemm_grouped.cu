@@ -811,7 +811,8 @@ cudaError_t launch_pair(const GroupedParams &p, int clusters, cudaStream_t s) {
 }
 
 // The host knows the rows of all experts together, not of each; blocks: what
-// they can need at most.
+// they can need at most.  (kernel_of in tests/test_gpu_experts.py restates the
+// rule, so that a case there names the kernel it is for.)
 //   K is split S ways while the items leave SMs idle (items S 2 <= SMs) and
 //   every CTA keeps two k-tiles, up to 4 (one token, 2 of 8 experts, MXFP8: 2048
 //   x 4096 8.4 against 15.4 us by pairs; 1024 x 2048 11.2 us with clusters of 8,

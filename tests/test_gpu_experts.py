@@ -355,6 +355,88 @@ def test_int8_part_of_the_experts_in_place(mxq, orc, counts, n, k):
         assert (z[:lo] == 3.0).all() and (z[hi:] == 3.0).all()
 
 
+def kernel_of(fmt, rows, groups, n, k):
+    """The kernel that launch_fmt (gemm_grouped.cu) picks for these sizes: "split", or a pair's row block and epilogue warps
+    per lane quarter.  To be kept in step with it: the tests below name the kernel they are for."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    k_tiles = -(-k // (256 if fmt in (MXFP4, NVFP4) else 128))
+    ragged = min(rows, groups)
+    items, split = (rows // 128 + ragged) * -(-n // 128), 1
+    while split < 4 and items * split * 2 <= sms and k_tiles >= split * 4:
+        split *= 2
+    if split > 1:
+        return "split"
+    wide = rows > 80 * groups
+    items = (rows // (256 if wide else 128) + ragged) * -(-n // 256)
+    if not wide:
+        return 128, 1
+    rounds_of_two = items <= 2 * min(items, sms // 2)
+    return 256, 1 if fmt in BLOCK and not rounds_of_two and k_tiles >= 8 else 2
+
+
+# counts, n, k (of 8-bit formats; twice that for 4 bits) and the kernel
+BY_KERNEL = [([5, 0, 2], 256, 4608, "split"), ([17, 128, 129, 0, 40, 1], 264, 320, (128, 1)),
+             ([60, 3, 128, 70, 0, 33], 4608, 1152, (128, 1)), ([500, 700, 3], 384, 320, (256, 2)),
+             ([300, 90, 257], 4608, 576, (256, 2)), ([600, 513, 256, 700, 257], 2816, 1024, (256, "many rounds"))]
+
+
+def kernel_wanted(fmt, kernel):
+    if kernel == (256, "many rounds"):   # one epilogue warp per quarter with block scales
+        return 256, 1 if fmt in BLOCK else 2
+    return kernel
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts,n,k,kernel", BY_KERNEL)
+def test_every_kernel_same_bits_twice_and_by_parts(mxq, orc, fmt, counts, n, k, kernel):
+    """Each kernel: against binary64, the same bits twice, and parts of the experts in place (offsets from the middle, only
+    their rows written)."""
+    k *= 2 if fmt in (MXFP4, NVFP4) else 1
+    ex = Experts(mxq, orc, fmt, counts, n, k, extra=3)
+    e, rows = len(counts), ex.xq.rows
+    assert kernel_of(fmt, rows, e, n, k) == kernel_wanted(fmt, kernel)
+    ex.check(mxq, torch.bfloat16)
+    ex.check(mxq, torch.float32)
+    y = ex.run(mxq, torch.float32)
+    assert torch.equal(y, ex.run(mxq, torch.float32))
+    wc = ex.w.codes.view(e, -1)
+    ws = None if ex.w.scales is None else ex.w.scales.view(e, -1)
+    for first, last in ((1, e), (0, e - 1)):
+        part = mxq.ExpertWeight(fmt, last - first, n, k, wc[first:last].flatten(),
+                                None if ws is None else ws[first:last].flatten(),
+                                None if ex.w.tensor_scales is None else ex.w.tensor_scales[first:last])
+        q = mxq.QTensor(fmt, mxq.MMA, rows, k, ex.xq.codes, ex.xq.scales, ex.xq.tensor_scale)
+        if fmt in BLOCK:   # scales laid out from the part's first group
+            sp, tile = (k // BLOCK[fmt] + 15) // 16 * 16, sum((c + 127) // 128 for c in counts[:first])
+            q.scales = torch.full((mxq.grouped_scales_bytes(fmt, rows, last - first, k),), 0xFF, dtype=torch.uint8, device="cuda")
+            src = ex.xq.scales[128 * sp * tile:][:q.scales.numel()]
+            q.scales[:src.numel()] = src
+        z = torch.full_like(y, 3.0)
+        mxq.qlinear_grouped(q, part, ex.offsets[first:last + 1], out=z)
+        assert mxq.check() == 0
+        lo, hi = int(ex.off[first]), int(ex.off[last])
+        assert (z[:lo] == 3.0).all() and (z[hi:] == 3.0).all()
+        gemm_close(z[lo:hi].cpu().numpy(), ex.ref[lo:hi])
+        if fmt == INT8_ROW or kernel_of(fmt, rows, last - first, n, k) != "split" != kernel:
+            assert torch.equal(z[lo:hi], y[lo:hi])   # K in one run: an element has its sums' order in any block
+
+
+@pytest.mark.parametrize("counts,n,k,kernel", BY_KERNEL)
+def test_int8_is_qlinear_bit_for_bit_in_every_kernel(mxq, orc, counts, n, k, kernel):
+    ex = Experts(mxq, orc, INT8_ROW, counts, n, k)
+    assert kernel_of(INT8_ROW, ex.xq.rows, len(counts), n, k) == kernel_wanted(INT8_ROW, kernel)
+    codes, scales = ex.xq.codes.view(-1, k), ex.xq.scales.view(-1, 4)
+    wc, ws = ex.w.codes.view(len(counts), n, k), ex.w.scales.view(len(counts), n * 4)
+    for dt in (torch.float32, torch.bfloat16):
+        y = ex.run(mxq, dt)
+        for e, c in enumerate(counts):
+            if c:
+                lo, hi = int(ex.off[e]), int(ex.off[e + 1])
+                a = mxq.QTensor(INT8_ROW, mxq.MMA, c, k, codes[lo:hi].clone(), scales[lo:hi].clone(), None)
+                b = mxq.QTensor(INT8_ROW, mxq.MMA, n, k, wc[e].clone(), ws[e].clone(), None)
+                assert torch.equal(mxq.qlinear(a, b, out_dtype=dt), y[lo:hi])
+
+
 @pytest.mark.parametrize("bad", [[0, 5, 3, 20], [-7, 2, 2, 20], [0, 4, 90, 20], [19, 4, 4, 4], [2 ** 31 - 1] * 4])
 @pytest.mark.parametrize("fmt", [MXFP8, INT8_ROW])
 @pytest.mark.parametrize("scale", [1, 40])
