@@ -437,6 +437,22 @@ def test_int8_is_qlinear_bit_for_bit_in_every_kernel(mxq, orc, counts, n, k, ker
                 assert torch.equal(mxq.qlinear(a, b, out_dtype=dt), y[lo:hi])
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n", [131, 100, 7])
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+def test_product_split_with_ragged_columns(mxq, orc, fmt, n, out_dtype):
+    """K split, N no multiple of 8: the elements of a row's last ones go one by one, and nothing behind y is touched."""
+    ex = Experts(mxq, orc, fmt, [5, 0, 2, 129], n, 2048, extra=1)
+    rows, used = ex.xq.rows, int(ex.off[-1])
+    assert kernel_of(fmt, rows, 4, n, 2048) == "split"
+    room = torch.full((rows * n + 1024,), 7.0, dtype=out_dtype, device="cuda")
+    y = room[:rows * n].view(rows, n)
+    mxq.qlinear_grouped(ex.xq, ex.w, ex.offsets, out=y)
+    assert mxq.check() == 0
+    assert (y[used:] == 7.0).all() and (room[rows * n:] == 7.0).all()
+    gemm_close(y[:used].float().cpu().numpy(), ex.ref, bf16_out=out_dtype == torch.bfloat16)
+
+
 @pytest.mark.parametrize("bad", [[0, 5, 3, 20], [-7, 2, 2, 20], [0, 4, 90, 20], [19, 4, 4, 4], [2 ** 31 - 1] * 4])
 @pytest.mark.parametrize("fmt", [MXFP8, INT8_ROW])
 @pytest.mark.parametrize("scale", [1, 40])
