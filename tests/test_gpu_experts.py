@@ -207,6 +207,55 @@ def test_quantize_rows_in_order_and_empty(mxq, orc, fmt):
     assert mxq.check() == 0
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("had", [0, 32])
+def test_quantize_rows_of_no_expert_set_no_scale(mxq, fmt, dtype, had):
+    """Tokens without a row, rows behind the last group and tokens of another part's experts, all 1e30 (a maximum drops a
+    NaN, not these), among ones near 1: the tensor scale, and everything else, is that of the others alone."""
+    rng = np.random.default_rng(fmt)
+    tokens, topk, n, cols = 90, 3, 10, 320
+    ids = routing(rng, tokens, topk, n, 0.2)
+    ids[rng.choice(tokens, 20, replace=False)] = -1
+    off, slot = ref_plan(ids, n)
+    x = rng.standard_normal((tokens, cols)).astype(np.float32)
+    offd, slotd = torch.from_numpy(off).cuda(), torch.from_numpy(slot).cuda()
+    for first, last in ((0, n), (3, 7), (9, 10)):
+        lo, hi = int(off[first]), int(off[last])
+        mine = (slot >= lo) & (slot < hi)
+        placed = mine.any(1)
+        xd = dev(np.where(placed[:, None], x, np.float32(1e30)), dtype)
+        q = filled(mxq, fmt, tokens * topk, last - first, cols)
+        mxq.quantize_grouped(xd, fmt, offd[first:last + 1], slotd, had, out=q)
+        # the part's rows, each token's choice within it, as rows in order: the library's own quantizer on them
+        src = np.zeros(hi - lo, np.int64)
+        for t, i in zip(*np.nonzero(mine)):
+            src[slot[t, i] - lo] = t
+        rows = xd[torch.from_numpy(src).cuda()]
+        want = mxq.quantize(rows, fmt, had)
+        assert torch.equal(q.codes.view(tokens * topk, -1)[lo:hi].flatten(), want.codes.view(torch.uint8).flatten())
+        assert (q.codes.view(tokens * topk, -1)[:lo] == 0xFF).all() and (q.codes.view(tokens * topk, -1)[hi:] == 0xFF).all()
+        if fmt in (NVFP4, FP8_TENSOR):
+            assert q.tensor_scale.item() == want.tensor_scale.item() < 1
+        if fmt in BLOCK:
+            sp = (cols // BLOCK[fmt] + 15) // 16 * 16
+            at = mma_offset(scale_rows(off[first:last + 1] - lo, hi - lo)[:, None], np.arange(cols // BLOCK[fmt])[None], sp)
+            np.testing.assert_array_equal(q.scales.cpu().numpy()[at].reshape(-1), want.scales.cpu().numpy().reshape(-1))
+        elif fmt == INT8_ROW:
+            s = q.scales.view(torch.float32)
+            assert torch.equal(s[lo:hi], want.scales.view(torch.float32))
+            assert (q.scales.view(-1, 4)[:lo] == 0xFF).all() and (q.scales.view(-1, 4)[hi:] == 0xFF).all()
+        # the same rows in order already (a second linear): 1e30 in the rows before and behind the groups
+        y = torch.full((tokens * topk, cols), 1e30, dtype=xd.dtype, device="cuda")
+        y[lo:hi] = rows
+        z = filled(mxq, fmt, tokens * topk, last - first, cols)
+        mxq.quantize_grouped(y, fmt, offd[first:last + 1], None, had, out=z)
+        assert torch.equal(z.codes, q.codes)
+        assert z.scales is None or torch.equal(z.scales, q.scales)
+        assert z.tensor_scale is None or torch.equal(z.tensor_scale, q.tensor_scale)
+    assert mxq.check() == 0
+
+
 # ------------------------------------------------------------------ products
 
 def deq64(q):
