@@ -474,9 +474,8 @@ __device__ __forceinline__ float group_max(float a) {
 // (bit h of i clear) into (a+c, a-c); stages h < 16 stay inside the lane,
 // stages h >= 16 pair lanes that differ in bit h/16.  Then every element is
 // multiplied by norm = RN(1/sqrt(b)) (hadamard_chunk computes it; a loop over
-// many chunks passes it in; hadamard_stages leaves it to its caller).  All
-// lanes of the warp must call this.
-__device__ __forceinline__ void hadamard_stages(float v[16], int b, int lane) {
+// many chunks passes it in).  All lanes of the warp must call this.
+__device__ __forceinline__ void hadamard_chunk_n(float v[16], int b, int lane, float norm) {
     // stage h = 1 inside the lane, element pairs (i, i + 1)
     if (b > 1) {
 #pragma unroll
@@ -522,9 +521,6 @@ __device__ __forceinline__ void hadamard_stages(float v[16], int b, int lane) {
             }
         }
     }
-}
-__device__ __forceinline__ void hadamard_chunk_n(float v[16], int b, int lane, float norm) {
-    hadamard_stages(v, b, lane);
     const float2 n2 = make_float2(norm, norm);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
