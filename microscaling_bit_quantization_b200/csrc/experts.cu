@@ -34,7 +34,8 @@ constexpr int kPlanThreads = 512;   // >= kMaxGroups: a thread per expert in the
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanOneBlock = 4096;
 constexpr int kPlanBlockRows = 1024;
-constexpr int kPlanMaxBlocks = 74;   // half the SMs: see plan_block_rows
+constexpr int kPlanMaxBlocks = 74;   // half of a B200's 148 SMs (see plan_block_rows); a constant, since the workspace's
+                                     // size is asked for without a device
 static_assert(kPlanThreads >= kMaxGroups, "one thread per expert");
 
 template <typename I>
@@ -452,8 +453,9 @@ __global__ void __launch_bounds__(kGqThreads, 4) k_quantize_grouped(const T *__r
     }
 }
 
-// INT8 per row: a warp per token; the first 8 chunks of a lane (rows up to
-// 4096 elements) stay in registers between the row maximum and the codes.
+// INT8 per row: a warp per token; the first 8 chunks of a lane in bf16, 4 in
+// fp32 (rows up to 4096 and 2048 elements), stay in registers between the row
+// maximum and the codes, what is behind them is read twice.
 template <typename T>
 __global__ void __launch_bounds__(kGqThreads) k_quantize_grouped_int8(const T *__restrict__ x, GroupedQuantArgs a) {
     constexpr int kKeep = sizeof(T) == 2 ? 8 : 4;

@@ -22,7 +22,7 @@
 //               copies it to TMEM: a tcgen05.cp holds up the thread that issues
 //               it, and NVFP4 has eight a stage (one token, 8 of 64 experts,
 //               2048 x 4096: 15.1 us with the MMA thread issuing them, 12.7 with
-//               a thread for each)
+//               a thread for each, 12.0 as the kernels now are)
 // Every wait is bounded; one that runs out latches the error word, the CTA
 // lets what is in flight land and exits.
 #include <cuda.h>
@@ -810,8 +810,9 @@ cudaError_t launch_pair(const GroupedParams &p, int clusters, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k_gemm_grouped_pair<F, NB, SP>, p);
 }
 
-// The host knows the rows of all experts together, not of each; blocks: what
-// they can need at most.  (kernel_of in tests/test_gpu_experts.py restates the
+// The host knows the rows of all experts together, not of each, and those by
+// capacity: dropped choices and, in a call on a part of the experts, the rows of
+// the others count as rows.  Blocks: what they can need at most.  (kernel_of in tests/test_gpu_experts.py restates the
 // rule, so that a case there names the kernel it is for.)
 //   K is split S ways while the items leave SMs idle (items S 2 <= SMs) and
 //   every CTA keeps two k-tiles, up to 4 (one token, 2 of 8 experts, MXFP8: 2048

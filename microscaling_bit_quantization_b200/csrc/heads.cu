@@ -15,13 +15,14 @@
 // floor(32 / U) heads at a time (a pass).  A warp's work is an item: up to
 // 16 passes over the q heads, or the k heads, of one token, so that a lane's
 // weights and angles, joined to one linear map, serve them all and pointers
-// only step; the items of all q come before those of all k.  Sums run over the U lanes by shuffles: butterflies where U is a
-// power of two, else a tree.
+// only step; the items of all q come before those of all k, so that the warps
+// of a block, and the last blocks, have equal ones.  Sums run over the U lanes
+// by shuffles: butterflies where U is a power of two, else a tree.
 // Bound: instruction issue and latency together (8192 tokens x 40 heads x 128
-// in bf16: 30.5 us, 5.5 TB/s, some 125 instructions per pass of 256 elements, 67% of
-// issue slots used; items of up to 8 passes 34 us, of 6 35: a short one waits
-// for its angles as long as a long one; a token's q and k items side by side,
-// unequal in a block and at the end, 35 us with 8 passes, 37 with 16).
+// in bf16: 30.5 us, 5.6 TB/s, some 125 instructions per pass of 256 elements, 67% of
+// issue slots used; items of up to 8 passes 32.5 us: a short one waits for its
+// angles as long as a long one).  Lane counts that are no power of two pay idle
+// lanes and the tree: 72 wide 25.5 us (58% of the copy rate), 64 wide 18.7 (70%).
 #include <cuda_runtime.h>
 
 #include "groups.cuh"
@@ -185,7 +186,8 @@ __device__ __forceinline__ Angles angles_of(const HeadArgs &h, int u, bool turne
     return a;
 }
 // (The angles are asked for before the weights: they hang on the position's
-// load and come from further away; in the other order bf16 took 41 us, not 37.)
+// load and come from further away; in the other order the same heads to MXFP8
+// behind a Hadamard rotation take 48.4 us, not 47.7, in bf16 30.6, not 30.5.)
 template <bool IL>
 __device__ __forceinline__ Turn turn_of(const float *w, int p0, int p1, bool turned, const Angles &angles) {
     float4 x = make_float4(1.0f, 1.0f, 1.0f, 1.0f), y = x;
@@ -323,7 +325,8 @@ struct HeadItem {
 
 template <typename T, int UNITS, bool IL>
 __global__ void __launch_bounds__(kHeadThreads, 8) k_qk_norm_rope(HeadKernelArgs a) {
-    // passes whose loads are in flight (bf16: 2 take 37 us, 8 43; fp32: 4 64 us)
+    // passes whose loads are in flight (8192 x 40 heads x 128 bf16: 4 30.5 us, 2 32.0, 8 40.7; 72 wide 2 25.5, 4 26.2;
+    // 128 wide fp32 2 54.4, 4 66.9)
     constexpr int kDepth = sizeof(T) == 2 && UNITS > 0 ? 4 : 2;
     const HeadArgs &h = a.h;
     const int lane = threadIdx.x & 31;
@@ -422,10 +425,11 @@ __device__ __forceinline__ void hadamard_heads(Pairs &v, int b, int lane) {
 // them so; pairs of halves go through shared memory (1 KB per warp), stored so
 // that both 16-byte reads give even and odd elements apart.  The head's factor
 // (with 1/sqrt(b) in it) is applied where the codes are formed.  Bound: instruction
-// issue (the same heads to MXFP8: 36 us, with a Hadamard rotation of 128 48 us,
-// some 270 instructions per pass and 80% of issue slots used; two passes unrolled
-// 67 us and the cross-lane stages as a loop 63 us where the kernel took 57:
-// the instructions have to fit the fetch and be few).
+// issue (the same heads to MXFP8: 35.5 us, with a Hadamard rotation of 128 47.7,
+// pairs of halves 37.0 and 56.8; some 270 instructions per pass with the rotation
+// and 80% of issue slots used; two passes unrolled 48.9 us and pairs of halves
+// 55.1, the cross-lane stages as a loop 56.4 and 58.9: the instructions have to
+// fit the fetch and be few).
 template <typename T, int F, int UNITS, bool IL>
 __global__ void __launch_bounds__(kHeadThreads, 7) k_qk_norm_rope_quantize(HeadKernelArgs a) {
     __shared__ __align__(16) float buf[IL ? 1 : kHeadWarps][IL ? 4 : 256];
