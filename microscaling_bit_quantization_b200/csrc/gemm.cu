@@ -112,42 +112,6 @@ struct GemmParams {
 
 // ------------------------------------------------------------------ PTX
 
-
-
-// 2-D tiled TMA load into this CTA's shared memory, completing on the
-// barrier at cluster address `bar` (either CTA of the pair).
-__device__ __forceinline__ void tma_load_pair(const CUtensorMap *map, void *dst, uint32_t bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
-
-// Arrive on the barrier at this offset in both CTAs once the issued MMAs complete.
-__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
-}
-// Arrive on this CTA's barrier once this thread's issued tcgen05 operations complete.
-__device__ __forceinline__ void tc_commit_self(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tc_cp_pair(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
-
-// Descriptor of one 512-byte scale-factor atom for tcgen05.cp (no swizzle,
-// 8 rows of 16 B per core matrix, core matrices 128 B apart).
-__device__ __forceinline__ uint64_t sdesc_sf(const void *p) {
-    uint64_t a = (smem_u32(p) >> 4) & 0x3FFFu;
-    return a | (8ull << 32) | (1ull << 46);
-}
-
 template <int KIND>
 __device__ __forceinline__ void mma_block_scaled(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
                                                  uint32_t sfa, uint32_t sfb) {
@@ -457,18 +421,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                         tc_fence_after();
                         for (int a = par; a < natoms; a += kSfWarps) {
                             const uint32_t base = group + SF_SLOT_COLS * (uint32_t)a;
-                            tc_cp_pair(base, sdesc_sf(sf + 512 * a));
-                            tc_cp_pair(base + 4, sdesc_sf(sf + 2048 + 512 * a));
-                            if (b_hi) tc_cp_pair(base + 8, sdesc_sf(sf + 4096 + 512 * a));
+                            tc_cp_pair(base, sdesc_atom(sf + 512 * a));
+                            tc_cp_pair(base + 4, sdesc_atom(sf + 2048 + 512 * a));
+                            if (b_hi) tc_cp_pair(base + 8, sdesc_atom(sf + 4096 + 512 * a));
                         }
-                        tc_commit_self(sfready + s);
+                        tc_commit_pair_self(sfready + s);
                     } else {
                         mbar_arrive_local(sfready + s);
                     }
                 }
             }
             if (*abort_flag) {
-                tc_commit_self(drain);
+                tc_commit_pair_self(drain);
                 mbar_wait(drain, 0, p.wait_ns);
             }
         }

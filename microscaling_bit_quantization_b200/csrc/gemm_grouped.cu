@@ -58,24 +58,6 @@ struct GroupedParams {
 
 // ---- pieces of both kernels; CG: cta_group, 1 or 2
 
-__device__ __forceinline__ void tma_load_2d(const CUtensorMap *map, void *dst, uint64_t *bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tc_cp(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
-// One 512-byte scale atom for tcgen05.cp: no swizzle, 8-row core matrices 128 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_atom(const void *p) {
-    return (uint64_t)((smem_u32(p) >> 4) & 0x3FFFu) | (8ull << 32) | (1ull << 46);
-}
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -305,29 +287,6 @@ struct Pair {
     static_assert(kStage % 1024 == 0 && kSmem <= 227 * 1024, "shared memory budget");
     static_assert(kAcc1 + NB <= (kAtoms ? kTmemSf : 512u) && kAcc1 + 32 * kShared >= (uint32_t)NB, "TMEM budget");
 };
-
-__device__ __forceinline__ void tma_load_pair(const CUtensorMap *map, void *dst, uint32_t bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-}
-// Arrive on the barrier at this offset in both CTAs once the issued MMAs complete.
-__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
-}
-__device__ __forceinline__ void tc_commit_pair_self(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tc_cp_pair(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
-}
 
 template <int F, int NB, int SP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair<F, NB, SP>::kThreads, 1)

@@ -83,13 +83,6 @@ struct IGroupParams {
     unsigned long long wait_ns;
 };
 
-__device__ __forceinline__ void tma_load_2d(const CUtensorMap *map, void *dst, uint64_t *bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-        : "memory");
-}
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -111,11 +104,6 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Arrive on this CTA's barrier once this thread's issued MMAs complete.
-__device__ __forceinline__ void tc_commit_1(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
 
 template <int GROUP>
 __global__ void __launch_bounds__(IG_THREADS, 1) k_gemm_igroup(const __grid_constant__ IGroupParams p) {
@@ -222,7 +210,7 @@ __global__ void __launch_bounds__(IG_THREADS, 1) k_gemm_igroup(const __grid_cons
                                     mma_e4m3(d, sdesc_sw128(sa + koff), sdesc_sw128(sb + koff), mm > 0);
                                 }
                             }
-                            tc_commit_1(bfull + b);
+                            tc_commit(bfull + b);
                             any = true;
                         }
                     }
@@ -231,11 +219,11 @@ __global__ void __launch_bounds__(IG_THREADS, 1) k_gemm_igroup(const __grid_cons
                         *abort_flag = 1;
                         break;
                     }
-                    tc_commit_1(empty + s);
+                    tc_commit(empty + s);
                 }
             }
             if (*abort_flag && any) {   // no MMA may be in flight when TMEM is released
-                tc_commit_1(drain);
+                tc_commit(drain);
                 mbar_wait(drain, 0, p.wait_ns);
             }
         }

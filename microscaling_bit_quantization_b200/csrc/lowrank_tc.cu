@@ -73,22 +73,11 @@ struct LrTcParams {
     unsigned long long wait_ns;
 };
 
-__device__ __forceinline__ void tma_load_x(const CUtensorMap *map, void *dst, uint64_t *bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-        : "memory");
-}
 __device__ __forceinline__ void mma_lt(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc));
-}
-__device__ __forceinline__ void commit_lt(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
 }
 // Asynchronous 16-byte store into a cluster peer's shared memory that counts
 // its bytes on the peer's mbarrier (complete_tx): no fence, no separate arrival.
@@ -188,7 +177,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) k_lowrank_tc(const __grid_const
             for (int u = 0; u < pre; u++) {
                 const int rt = cid + (u / nkb) * ncl, kb = kb0 + u % nkb;
                 mbar_arrive_expect_tx(full + u, LT_X);
-                tma_load_x(&p.tma_x, xst + u * LT_X, full + u, kb * 64, rt * 128);
+                tma_load_2d(&p.tma_x, xst + u * LT_X, full + u, kb * 64, rt * 128);
             }
         }
     };
@@ -197,7 +186,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) k_lowrank_tc(const __grid_const
         // zeros past K): no transpose
         if (warp == 0 && lane == 0) {
             mbar_arrive_expect_tx(bfull, (uint32_t)(nkb * LT_B));
-            for (int j = 0; j < nkb; j++) tma_load_x(&p.tma_l1, btile + j * LT_B, bfull, 0, (kb0 + j) * 64);
+            for (int j = 0; j < nkb; j++) tma_load_2d(&p.tma_l1, btile + j * LT_B, bfull, 0, (kb0 + j) * 64);
         }
         prefetch_x();
     } else if (p.r % 8 == 0 && (reinterpret_cast<uintptr_t>(p.l1) & 15u) == 0) {
@@ -271,7 +260,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) k_lowrank_tc(const __grid_const
                 }
                 const int rt = cid + (u / nkb) * ncl, kb = kb0 + u % nkb;
                 mbar_arrive_expect_tx(full + s, LT_X);
-                tma_load_x(&p.tma_x, xst + s * LT_X, full + s, kb * 64, rt * 128);
+                tma_load_2d(&p.tma_x, xst + s * LT_X, full + s, kb * 64, rt * 128);
                 issued = u + 1;
             }
             if (*abort_flag) {   // let the copies in flight land
@@ -304,7 +293,7 @@ __global__ void __launch_bounds__(LT_THREADS, 1) k_lowrank_tc(const __grid_const
                         mma_lt(tmem + slot * 32, sdesc_sw128(xst + s * LT_X + ks * 32),
                                bmn ? sdesc_mn_sw64(btile + j * LT_B + ks * 1024) : sdesc_sw128(btile + j * LT_B + ks * 32),
                                idesc, (j > 0 || ks > 0) ? 1u : 0u);
-                    commit_lt(empty + s);
+                    tc_commit(empty + s);
                     any = true;
                 }
                 if (!ok) {
@@ -312,10 +301,10 @@ __global__ void __launch_bounds__(LT_THREADS, 1) k_lowrank_tc(const __grid_const
                     *abort_flag = 1;
                     break;
                 }
-                commit_lt(accf + slot);
+                tc_commit(accf + slot);
             }
             if (*abort_flag && any) {   // nothing may be in flight when TMEM is released
-                commit_lt(drain);
+                tc_commit(drain);
                 mbar_wait(drain, 0, p.wait_ns);
             }
         }

@@ -59,22 +59,11 @@ struct W4a16Params {
     unsigned long long wait_ns;
 };
 
-__device__ __forceinline__ void tma_load_a(const CUtensorMap *map, void *dst, uint64_t *bar, int c0, int c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-        : "memory");
-}
 __device__ __forceinline__ void mma_wa(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(kWaIdesc), "r"(acc));
-}
-__device__ __forceinline__ void commit_wa(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
 }
 
 // Eight signed 4-bit codes (one word, element 2i in the low nibble of byte i)
@@ -166,7 +155,7 @@ __global__ void __launch_bounds__(WA_THREADS, 1) k_w4a16(const __grid_constant__
                 }
                 const int tile = (int)blockIdx.x + (u / p.kb_total) * (int)gridDim.x, kb = u % p.kb_total;
                 mbar_arrive_expect_tx(afull + s, WA_A);
-                tma_load_a(&p.tma_x, smem + s * WA_STAGE, afull + s, kb * 64, (tile / p.n_tiles) * 128);
+                tma_load_2d(&p.tma_x, smem + s * WA_STAGE, afull + s, kb * 64, (tile / p.n_tiles) * 128);
                 issued = u + 1;
             }
             if (*abort_flag) {   // let the copies in flight land
@@ -194,7 +183,7 @@ __global__ void __launch_bounds__(WA_THREADS, 1) k_w4a16(const __grid_constant__
                     for (int ks = 0; ks < 4; ks++)
                         mma_wa(tmem + slot * 128, sdesc_sw128(sa + ks * 32), sdesc_sw128(sa + WA_A + ks * 32),
                                (kb > 0 || ks > 0) ? 1u : 0u);
-                    commit_wa(empty + s);
+                    tc_commit(empty + s);
                     any = true;
                 }
                 if (!ok || *abort_flag) {
@@ -202,10 +191,10 @@ __global__ void __launch_bounds__(WA_THREADS, 1) k_w4a16(const __grid_constant__
                     *abort_flag = 1;
                     break;
                 }
-                commit_wa(accf + slot);
+                tc_commit(accf + slot);
             }
             if (*abort_flag && any) {   // nothing may be in flight when TMEM is released
-                commit_wa(drain);
+                tc_commit(drain);
                 mbar_wait(drain, 0, p.wait_ns);
             }
         }
