@@ -637,7 +637,9 @@ mxq_status mxq_qlinear_routed(const void *x, int32_t xdtype, int64_t m, int64_t 
  * that hold no scale are unspecified.  Codes and INT8_ROW scales are compact.
  * A part of the experts: pass offsets + first, n_groups = count and the
  * weight of those experts; slots outside [offsets[first],
- * offsets[first + count]) are passed over.
+ * offsets[first + count]) are passed over.  (mxq_expert_combine takes no
+ * offsets: it reads every row that slot names, so the rows of the other parts
+ * have to hold their products by then, or zeros.)
  * Limits: rows <= 2^22, 1 <= experts <= 512, 1 <= topk <= 32, byte scales
  * below 2^34 bytes.
  * Offsets are device data: ones outside [0, rows] or out of order are
@@ -720,8 +722,11 @@ mxq_status mxq_expert_weight_prepare(const void *w, int32_t wdtype, int32_t hada
  *   offsets: device int32[w->n_experts + 1], those xq was written with.
  *   y: xq->rows x w->rows device, fp32 or bf16, 16-byte aligned.
  * Constraints: K % 64 == 0 (4 bits) or K % 32 == 0 (8 bits); K <= 133,144 for
- * INT8_ROW; pointers 16-byte aligned, fp32 scales, tensor scales and offsets
- * 4-byte aligned.  Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED (format, format pair),
+ * INT8_ROW; with n = ceil(N / 128), T = xq->rows / 128 + min(xq->rows,
+ * n_experts) and k = K / 16: n_experts * (n + 1) * 128, n_experts * n * k / 4,
+ * T * n * k and T * k / 4 below 2^31 (k rounded up to 16 in the quotients);
+ * pointers 16-byte aligned, fp32 scales, tensor scales and offsets 4-byte
+ * aligned.  Errors: MXQ_EINVAL, MXQ_EUNSUPPORTED (format, format pair),
  * MXQ_ECUDA; a pipeline wait that runs out is reported by mxq_check(). */
 mxq_status mxq_qlinear_grouped(const mxq_qtensor *xq, const int32_t *offsets, const mxq_expert_weight *w,
                                void *y, int32_t ydtype, void *stream);
@@ -752,7 +757,7 @@ typedef enum mxq_norm { MXQ_NORM_RMS = 0, MXQ_NORM_LAYER = 1 } mxq_norm;
 typedef struct mxq_heads {
     const void *q, *k;             /* device, 16-byte aligned (NULL when it has no heads) */
     int64_t q_stride, k_stride;    /* multiples of 8                          */
-    int32_t q_heads, k_heads;
+    int32_t q_heads, k_heads;      /* 0 .. 65,536                             */
     int32_t head_dim;              /* multiple of 8, 8 .. 256                 */
     int32_t dtype;                 /* mxq_dtype of q and k                    */
     int64_t tokens;                /* below 2^30                              */
@@ -772,7 +777,8 @@ typedef struct mxq_heads {
  *   for x, the mean square of that), then for the pairs (a, b) of the first
  *   rot_dim elements a' = a c - b s, b' = b c + a s with c, s of the token's
  *   position and pair; fp32, rounded once (RNE) for bf16 (sums of squares, and
- *   products of an element and its weight, beyond 3.4e38 overflow).
+ *   products of an element and its weight, beyond 3.4e38 overflow; squares
+ *   below 1e-45 are zero, which shows where eps is about as small).
  *   q_out, k_out: device, dtype of h, strides in elements as q and k; q_out
  *     may be q (same stride), k_out may be k.
  * A head with a NaN is NaN; one with an infinite element is NaN there and at

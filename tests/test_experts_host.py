@@ -225,3 +225,23 @@ def test_int8_sums_that_could_leave_int32_are_refused(mxq):
         assert f(M.INT8_ROW, bad) == EINVAL and f(M.INT8_ROW, bad, 8) == EINVAL
         assert f(M.FP8_TENSOR, bad) == 0
     assert L.mxq_expert_weight_prepare(D, 1, 0, ctypes.byref(weight(M, fmt=M.INT8_ROW, cols=bad)), None, 0, None) == EINVAL
+
+
+def test_limits_the_header_states(mxq):
+    """Each index limit of the grouped product, one step on either side (no rows, or no columns, where accepted)."""
+    M, f = mxq, mxq.lib().mxq_qlinear_grouped
+
+    def call(fmt, rows, e, n, k):
+        q = M._QTensorC(fmt, M.MMA, rows, k, D, D, D)
+        return f(ctypes.byref(q), D, ctypes.byref(weight(M, fmt=fmt, e=e, rows=n, cols=k)), D, 1, None)
+
+    # experts' padded rows: 512 * (n + 1) * 128 < 2^31
+    assert call(M.MXFP8, 0, 512, 32766 * 128, 64) == 0 and call(M.MXFP8, 0, 512, 32766 * 128 + 1, 64) == EINVAL
+    # experts' scale atoms: 512 * n * (k / 4) < 2^31 with k = 2^14
+    assert call(M.MXFP8, 0, 512, 1023 * 128, 1 << 18) == 0 and call(M.MXFP8, 0, 512, 1024 * 128, 1 << 18) == EINVAL
+    # items and their K stages: T * n * k < 2^31 with T = 2^15 + 1
+    assert call(M.MXFP8, 1 << 22, 1, 512 * 128, 2048) == EINVAL
+    assert call(M.MXFP8, 1 << 22, 1, 0, 2048) == 0
+    L, more = mxq.lib(), dict(q=D, k=D, head_dim=8, dtype=1, tokens=1, norm=0, eps=1e-6, k_heads=1, k_stride=8)
+    h = Heads(**{**more, "q_heads": 65537, "q_stride": 1 << 20})
+    assert L.mxq_qk_norm_rope(ctypes.byref(h), D, 1 << 20, D, 8, None) == EINVAL
