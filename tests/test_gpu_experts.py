@@ -256,6 +256,38 @@ def test_quantize_rows_of_no_expert_set_no_scale(mxq, fmt, dtype, had):
     assert mxq.check() == 0
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("had,cols", [(0, 320), (64, 320), (0, 5120)])
+def test_quantize_inputs_that_are_no_numbers(mxq, fmt, dtype, had, cols):
+    """NaN, infinities and the largest values: the bits of mxq_quantize, whatever they are, in the right rows; a token that
+    names one expert twice, and room for more rows than there are."""
+    rng = np.random.default_rng(fmt)
+    tokens, topk, n = 40, 3, 6
+    x = rng.standard_normal((tokens, cols)).astype(np.float32)
+    if fmt not in (NVFP4, FP8_TENSOR):   # (one such value sets the scale of the whole tensor)
+        x[3, 7], x[5, 30:70], x[9], x[11, 100], x[12, 0], x[13] = np.nan, np.nan, np.nan, np.inf, -np.inf, np.inf
+        x[14, 3], x[14, 4], x[20], x[21, 5] = np.inf, -np.inf, 3e38, -3.3e38
+    x[22], x[23, :32] = 0.0, 1e-40
+    ids = rng.integers(-1, n, (tokens, topk))
+    ids[:, 0] = np.arange(tokens) % n
+    ids[7] = 2
+    off, slot = ref_plan(ids, n)
+    xd = dev(x, dtype)
+    q = filled(mxq, fmt, tokens * topk + 33, n, cols)
+    mxq.quantize_grouped(xd, fmt, torch.from_numpy(off).cuda(), torch.from_numpy(slot).cuda(), had, out=q)
+    assert mxq.check() == 0
+    lib = mxq.quantize(xd, fmt, had)
+    sc = None if lib.scales is None else lib.scales.cpu().numpy()
+    same = Bits(lib.codes.cpu().numpy().reshape(tokens, -1),
+                sc.reshape(tokens, -1) if fmt in BLOCK else None if sc is None else sc.view(np.float32),
+                None if lib.tensor_scale is None else lib.tensor_scale.item(), tokens)
+    src = np.zeros(int(off[-1]), np.int64)
+    for t, i in zip(*np.nonzero(slot >= 0)):
+        src[slot[t, i]] = t
+    check_grouped(q, same, fmt, off, src, 0xFF)
+
+
 # ------------------------------------------------------------------ products
 
 def deq64(q):
@@ -500,6 +532,41 @@ def test_product_split_with_ragged_columns(mxq, orc, fmt, n, out_dtype):
     assert mxq.check() == 0
     assert (y[used:] == 7.0).all() and (room[rows * n:] == 7.0).all()
     gemm_close(y[:used].float().cpu().numpy(), ex.ref, bf16_out=out_dtype == torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts,n,k", [([5, 0, 130], 136, 320), ([3, 2], 100, 2048), ([700, 300], 264, 320)])
+def test_product_of_rotated_operands(mxq, orc, fmt, counts, n, k):
+    """Both sides quantized behind the Hadamard rotation: the product of what the oracle's rotated codes stand for."""
+    ex = Experts(mxq, orc, fmt, counts, n, k, extra=2, had=64)
+    ex.check(mxq, torch.float32)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts,n,k", [([5, 0, 130, 2], 136, 2048), ([70, 3, 128, 90], 264, 320), ([700, 3, 300], 264, 320)])
+def test_product_keeps_a_nan_where_it_is(mxq, orc, fmt, counts, n, k):
+    """A row of X, and a feature of one expert, that hold a NaN: their row and column of y, and no other element."""
+    if fmt in (MXFP4, NVFP4):
+        k *= 2
+    ex = Experts(mxq, orc, fmt, counts, n, k)
+    y = ex.run(mxq, torch.float32)
+    row, feature, rows = 4, 37, ex.xq.rows
+    if fmt in BLOCK:   # a NaN block scale: 0xFF in E8M0, 0x7F in E4M3
+        sp = (k // BLOCK[fmt] + 15) // 16 * 16
+        bad = 0x7F if fmt == NVFP4 else 0xFF
+        ex.xq.scales[int(mma_offset(row, 3, sp))] = bad
+        ex.w.scales.view(len(counts), -1)[2, int(mma_offset(feature, 1, sp))] = bad
+    elif fmt == INT8_ROW:
+        ex.xq.scales.view(torch.float32)[row] = float("nan")
+        ex.w.scales.view(torch.float32).view(len(counts), n)[2, feature] = float("nan")
+    else:
+        ex.xq.codes.view(rows, k)[row, 3] = 0x7F
+        ex.w.codes.view(len(counts), n, k)[2, feature, 40] = 0x7F
+    z = ex.run(mxq, torch.float32)
+    nan = torch.zeros(rows, n, dtype=torch.bool, device="cuda")
+    nan[row] = True
+    nan[int(ex.off[2]):int(ex.off[3]), feature] = True
+    assert torch.equal(torch.isnan(z), nan) and torch.equal(z[~nan], y[~nan])
 
 
 @pytest.mark.parametrize("bad", [[0, 5, 3, 20], [-7, 2, 2, 20], [0, 4, 90, 20], [19, 4, 4, 4], [2 ** 31 - 1] * 4])
