@@ -330,3 +330,39 @@ def test_codes_keep_nan(mxq, fmt, interleaved, d, rot, had, dtype, norm):
     assert all(b.any(1).all() for b in bad)
     check(coded(q, k, w), bad)
     assert mxq.check() == 0
+
+
+@pytest.mark.parametrize("fmt", [None, MXFP8, MXFP4, INT8_ROW])
+def test_heads_captured_strided_and_on_another_stream(mxq, fmt):
+    """A captured call replayed on other inputs and positions; every second token of a longer buffer; a stream of its own."""
+    t, hq, hk, d = 70, 6, 2, 96
+    g = torch.Generator("cuda").manual_seed(9)
+    big = torch.randn(2 * t, (hq + hk) * d, device="cuda", generator=g).bfloat16()
+    q, k = big[::2, :hq * d].unflatten(1, (hq, d)), big[::2, hq * d:].unflatten(1, (hk, d))
+    w = torch.rand(d, device="cuda", generator=g)
+    cos, sin = (torch.from_numpy(a).cuda() for a in tables(50, 64))
+    pos = torch.randint(0, 50, (t,), device="cuda", generator=g)
+
+    def f(q, k, stream=None):
+        if fmt is None:
+            return list(mxq.qk_norm_rope(q, k, w, w, cos, sin, pos, norm="layer", stream=stream))
+        out = mxq.qk_norm_rope_quantize(q, k, w, w, cos, sin, pos, norm="layer", fmt=fmt, hadamard_b=32, stream=stream)
+        return [x for o in out for x in (o.codes, o.scales)]
+
+    same = lambda a, b: all(torch.equal(x, y) for x, y in zip(a, b))  # noqa: E731
+    assert same(f(q, k), f(q.contiguous(), k.contiguous()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = f(q, k, stream=side)
+    torch.cuda.synchronize()
+    assert same(other, f(q, k))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+        out = f(q, k)
+    for _ in range(3):
+        big.copy_(torch.randn(big.shape, device="cuda", generator=g))
+        pos.copy_(torch.randint(0, 50, (t,), device="cuda", generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out, f(q, k))
+    assert mxq.check() == 0
